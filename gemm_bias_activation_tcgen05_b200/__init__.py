@@ -9,7 +9,8 @@ without a B200.
 The entry points keep the C names: ``fl_plan``, ``fl_execute``, ``fl_free``,
 ``fl_relu_backward``, ``fl_check_status``, ``fl_get_plan_info``,
 ``fl_last_error``, ``fl_set_wait_limit_ns``, ``fl_execute_noalloc``, ``fl_bias_grad_workspace_size``,
-``fl_drelu_bgrad``, ``fl_dgelu_bgrad``, ``fl_layernorm``, ``fl_wait_selftest``, ``fl_plan_preview``.
+``fl_drelu_bgrad``, ``fl_dgelu_bgrad``, ``fl_layernorm``, ``fl_wait_selftest``, ``fl_plan_preview``, ``fl_dropout``,
+``fl_dropout_layernorm``, ``fl_layernorm_grad_workspace_size``, ``fl_dropout_layernorm_backward``.
 ``Plan`` is a small owner of one plan handle (the cuBLASLt epilog page's Matmul → plan → execute → free).
 """
 from __future__ import annotations
@@ -38,7 +39,8 @@ SCHEDULES = {"auto": 0, "data_parallel": 1, "stream_k": 2}
 EXPORTED = ["fl_plan", "fl_execute", "fl_relu_backward", "fl_check_status", "fl_get_plan_info",
             "fl_free", "fl_last_error", "fl_set_wait_limit_ns", "fl_execute_noalloc",
             "fl_bias_grad_workspace_size", "fl_drelu_bgrad", "fl_dgelu_bgrad", "fl_layernorm", "fl_wait_selftest",
-            "fl_plan_preview"]
+            "fl_plan_preview", "fl_dropout", "fl_dropout_layernorm", "fl_layernorm_grad_workspace_size",
+            "fl_dropout_layernorm_backward"]
 
 
 class fl_epilogue_desc(ctypes.Structure):
@@ -57,6 +59,11 @@ class fl_plan_info(ctypes.Structure):
                 ("launches_per_execute", ctypes.c_int32), ("cta_pair", ctypes.c_int32),
                 ("stream_k_tiles", ctypes.c_int32), ("stream_k_pairs", ctypes.c_int32),
                 ("reserved", ctypes.c_int32 * 4)]
+
+
+class fl_dropout_desc(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("reserved", ctypes.c_int32), ("seed", ctypes.c_uint64),
+                ("offset", ctypes.c_uint64), ("offset_dev", ctypes.c_void_p)]
 
 
 def _load() -> ctypes.CDLL:
@@ -98,6 +105,15 @@ def _load() -> ctypes.CDLL:
     lib.fl_layernorm.restype = i32
     lib.fl_wait_selftest.argtypes = [ctypes.c_uint64, vp]
     lib.fl_wait_selftest.restype = i32
+    dp = ctypes.POINTER(fl_dropout_desc)
+    lib.fl_dropout.argtypes = [vp, vp, vp, *[i64] * 5, i32, i32, dp, vp]
+    lib.fl_dropout.restype = i32
+    lib.fl_dropout_layernorm.argtypes = [*[vp] * 8, *[i64] * 6, *[i32] * 4, ctypes.c_float, dp, vp]
+    lib.fl_dropout_layernorm.restype = i32
+    lib.fl_layernorm_grad_workspace_size.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t)]
+    lib.fl_layernorm_grad_workspace_size.restype = i32
+    lib.fl_dropout_layernorm_backward.argtypes = [*[vp] * 10, *[i64] * 7, *[i32] * 4, dp, vp, ctypes.c_size_t, vp]
+    lib.fl_dropout_layernorm_backward.restype = i32
     return lib
 
 
@@ -215,6 +231,49 @@ def fl_layernorm(x, gamma, beta, z, M: int, N: int, x_dtype: str, z_dtype: str, 
     _check(LIB.fl_layernorm(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(z), int(M), int(N), int(ld_x), int(ld_z),
                             DTYPES[x_dtype], DTYPES[z_dtype], DTYPES[param_dtype], float(eps), _stream(stream)),
            "fl_layernorm")
+
+
+def _dropout(p: float, seed: int, offset: int, offset_dev):
+    """The dropout descriptor; seed and offset are taken modulo 2^64."""
+    return ctypes.byref(fl_dropout_desc(float(p), 0, int(seed) % 2**64, int(offset) % 2**64, _ptr(offset_dev)))
+
+
+def fl_dropout(x, residual, y, M: int, N: int, x_dtype: str, y_dtype: str, p: float = 0.0, seed: int = 0,
+               offset: int = 0, offset_dev=None, ld_x: int = 0, ld_r: int = 0, ld_y: int = 0, stream=None) -> None:
+    """y = residual + dropout(x); also the backward of dropout, with the same seed and offset."""
+    _check(LIB.fl_dropout(_ptr(x), _ptr(residual), _ptr(y), int(M), int(N), int(ld_x), int(ld_r), int(ld_y),
+                          DTYPES[x_dtype], DTYPES[y_dtype], _dropout(p, seed, offset, offset_dev), _stream(stream)),
+           "fl_dropout")
+
+
+def fl_dropout_layernorm(x, residual, gamma, beta, sum, z, mean, rstd, M: int, N: int, x_dtype: str, sum_dtype: str,
+                         z_dtype: str, param_dtype: str = "f32", eps: float = 1e-12, p: float = 0.0, seed: int = 0,
+                         offset: int = 0, offset_dev=None, ld_x: int = 0, ld_r: int = 0, ld_sum: int = 0,
+                         ld_z: int = 0, stream=None) -> None:
+    """sum = residual + dropout(x) and z = LayerNorm(sum), with the row statistics the backward reads."""
+    _check(LIB.fl_dropout_layernorm(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(beta), _ptr(sum), _ptr(z), _ptr(mean),
+                                    _ptr(rstd), int(M), int(N), int(ld_x), int(ld_r), int(ld_sum), int(ld_z),
+                                    DTYPES[x_dtype], DTYPES[sum_dtype], DTYPES[z_dtype], DTYPES[param_dtype],
+                                    float(eps), _dropout(p, seed, offset, offset_dev), _stream(stream)),
+           "fl_dropout_layernorm")
+
+
+def fl_layernorm_grad_workspace_size(M: int, N: int) -> int:
+    n = ctypes.c_size_t()
+    _check(LIB.fl_layernorm_grad_workspace_size(int(M), int(N), ctypes.byref(n)), "fl_layernorm_grad_workspace_size")
+    return int(n.value)
+
+
+def fl_dropout_layernorm_backward(dz, dsum, sum, mean, rstd, gamma, dres, dx, dgamma, dbeta, M: int, N: int,
+                                  x_dtype: str, sum_dtype: str, z_dtype: str, param_dtype: str = "f32",
+                                  workspace=None, workspace_bytes: int = 0, p: float = 0.0, seed: int = 0,
+                                  offset: int = 0, offset_dev=None, ld_dz: int = 0, ld_dsum: int = 0, ld_sum: int = 0,
+                                  ld_dres: int = 0, ld_dx: int = 0, stream=None) -> None:
+    _check(LIB.fl_dropout_layernorm_backward(
+        _ptr(dz), _ptr(dsum), _ptr(sum), _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(dres), _ptr(dx), _ptr(dgamma),
+        _ptr(dbeta), int(M), int(N), int(ld_dz), int(ld_dsum), int(ld_sum), int(ld_dres), int(ld_dx), DTYPES[x_dtype],
+        DTYPES[sum_dtype], DTYPES[z_dtype], DTYPES[param_dtype], _dropout(p, seed, offset, offset_dev),
+        _ptr(workspace), int(workspace_bytes), _stream(stream)), "fl_dropout_layernorm_backward")
 
 
 def fl_wait_selftest(limit_ns: int, stream=None) -> int:

@@ -3,10 +3,13 @@
 The library holds the C ABI of ``include/fused_linear.h`` and every CUDA
 kernel of the fused linear layer.  It links the CUDA runtime statically and
 reaches the driver's tensor-map encoder through the runtime's driver entry
-point, so loading it needs no libcuda at link time.
+point, so loading it needs no libcuda at link time.  Each source is compiled to
+an object of its own, several at a time; an object whose sources have not changed
+is kept.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
@@ -15,9 +18,22 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libfused_linear.so")
-SOURCES = [os.path.join(HERE, "csrc", "fl_api.cu")]
-DEPS = SOURCES + [os.path.join(HERE, "csrc", f) for f in ("fl_gemm.cuh", "fl_ptx.cuh", "fl_elementwise.cuh")] + \
-    [os.path.join(ROOT, "include", "fused_linear.h")]
+OBJ_DIR = os.path.join(HERE, "_build")
+_GEMM = ["fl_gemm.cuh", "fl_ptx.cuh", "fl_host.h"]
+# each translation unit and the headers it includes
+UNITS = {
+    "fl_api.cu": ["fl_elementwise.cuh", *_GEMM],
+    "fl_rows.cu": ["fl_rows.cuh", *_GEMM],
+}
+HEADER = os.path.join(ROOT, "include", "fused_linear.h")
+
+
+def _src(name: str) -> str:
+    return os.path.join(HERE, "csrc", name)
+
+
+SOURCES = [_src(u) for u in UNITS]
+DEPS = sorted({_src(f) for u, hs in UNITS.items() for f in (u, *hs)}) + [HEADER]
 
 
 def nvcc() -> str:
@@ -27,31 +43,63 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def command(extra=()):
-    return [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-            "--shared", "-Xcompiler", "-fPIC", "-cudart", "static", "-Xptxas", "-v",
-            f"-I{os.path.join(ROOT, 'include')}", *extra, *SOURCES, "-o", LIB]
+def _flags():
+    return ["-gencode", "arch=compute_100a,code=sm_100a", "-Xcompiler", "-fPIC", "-cudart", "static"]
+
+
+def _object(unit: str) -> str:
+    return os.path.join(OBJ_DIR, unit.replace(".cu", ".o"))
+
+
+def compile_command(unit: str):
+    return [nvcc(), *_flags(), "-lineinfo", "-O3", "-std=c++17", "-Xptxas", "-v",
+            f"-I{os.path.join(ROOT, 'include')}", "-c", _src(unit), "-o", _object(unit)]
+
+
+def link_command():
+    return [nvcc(), *_flags(), "--shared", *[_object(u) for u in UNITS], "-o", LIB]
+
+
+def _newer(target: str, deps) -> bool:
+    if not os.path.exists(target):
+        return False
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(d) <= t for d in deps)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in DEPS)
+    return _newer(LIB, DEPS)
+
+
+def _compile(unit: str, force: bool) -> str:
+    """Compile one unit unless its object is current; its resource report (ptxas -v)."""
+    report = _object(unit) + ".txt"
+    deps = [_src(f) for f in (unit, *UNITS[unit])] + [HEADER]
+    if not force and os.path.exists(report) and _newer(_object(unit), deps):
+        return open(report).read()
+    r = subprocess.run(compile_command(unit), capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"nvcc failed compiling {unit}")
+    with open(report, "w") as f:
+        f.write(r.stderr)
+    return r.stderr
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
-    cmd = command()
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(UNITS), os.cpu_count() or 1))) as ex:
+        reports = list(ex.map(lambda u: _compile(u, force), UNITS))
+    r = subprocess.run(link_command(), capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc failed building libfused_linear.so")
+        raise RuntimeError("nvcc failed linking libfused_linear.so")
     with open(os.path.join(HERE, "ptxas_report.txt"), "w") as f:
-        f.write(r.stderr)
+        f.write("".join(reports))
     if verbose:
-        sys.stderr.write(r.stderr)
+        sys.stderr.write("".join(reports))
     return LIB
 
 

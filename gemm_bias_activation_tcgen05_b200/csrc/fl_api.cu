@@ -20,25 +20,23 @@
 #include "../../include/fused_linear.h"
 #include "fl_elementwise.cuh"
 #include "fl_gemm.cuh"
+#include "fl_host.h"
 
 using namespace fl;
+using namespace fl::host;
 
 // ------------------------------------------------------------------ errors
 static thread_local char g_err[512] = "";
 static uint64_t g_wait_limit_ns = 2000000000ull;
 
-static fl_status fail(fl_status st, const char* fmt, ...) {
+fl_status fl::host::fail(fl_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_err, sizeof(g_err), fmt, ap);
   va_end(ap);
   return st;
 }
-#define FL_CUDA(call)                                                                      \
-  do {                                                                                     \
-    cudaError_t e_ = (call);                                                               \
-    if (e_ != cudaSuccess) return fail(FL_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_)); \
-  } while (0)
+void fl::host::clear_error() { g_err[0] = 0; }
 
 extern "C" const char* fl_last_error(void) { return g_err; }
 
@@ -63,8 +61,6 @@ static fl_status get_encode() {
   return FL_OK;
 }
 
-static int esize(int dt) { return dt == FL_F32 ? 4 : 2; }
-
 // FL_SYNC_EACH_LAUNCH=1 (debug only): synchronise after every launch and name
 // the launch whose execution failed.
 static bool sync_each_launch() {
@@ -74,7 +70,7 @@ static bool sync_each_launch() {
   }();
   return on;
 }
-static fl_status after_launch(cudaStream_t s, const char* what) {
+fl_status fl::host::after_launch(cudaStream_t s, const char* what) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(FL_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
   if (sync_each_launch()) {
@@ -91,14 +87,15 @@ static CUtensorMapDataType tm_dtype(int dt) {
 }
 
 // 2-D row-major map: `inner` contiguous elements per row, `outer` rows, row pitch in bytes.
-static fl_status make_map(CUtensorMap* m, const void* base, int dt, uint64_t inner, uint64_t outer,
-                          uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer) {
+fl_status fl::host::make_map(CUtensorMap* m, const void* base, int dt, uint64_t inner, uint64_t outer,
+                             uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer, bool swizzle64) {
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {pitch_bytes};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = g_encode(m, tm_dtype(dt), 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(FL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d): dims %llu x %llu pitch %llu box %u x %u",
@@ -235,8 +232,6 @@ static int act_of(int kind) {
     default: return ACT_NONE;
   }
 }
-
-static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Shared-memory layout of one configuration: the operand ring, then (normal
 // layout) the epilogue staging buffers and per-warp bias rows, then (split-K)
@@ -725,8 +720,6 @@ extern "C" fl_status fl_free(fl_plan_t p) {
   return FL_OK;
 }
 
-static bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-
 // ------------------------------------------------------------------ launch helpers
 struct GemmArgs {
   const void* A;
@@ -743,22 +736,7 @@ struct GemmArgs {
   bool geglu_fused;
 };
 
-// Launch an elementwise kernel with programmatic dependent launch allowed.
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_pdl_b(void (*kern)(KArgs...), dim3 grid, unsigned block, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block, 1, 1);
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
+// Launch a 256-thread elementwise kernel with programmatic dependent launch allowed.
 template <typename... KArgs, typename... Args>
 static cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, cudaStream_t s, Args... args) {
   return launch_pdl_b(kern, grid, 256u, s, args...);

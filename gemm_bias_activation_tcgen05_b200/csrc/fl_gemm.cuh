@@ -269,7 +269,7 @@ __device__ __forceinline__ void sk_add_block(float* x, const float* area, int bl
 // keeps its allocation): the warp's accumulator blocks b = 0 .. mma_n/64 - 1 sit at TMEM
 // column c_begin + 32b, or, past gblk blocks (GeGLU's up half), out_tile_n + c_begin +
 // 32(b - gblk).
-__device__ __noinline__ void sk_store_partial(const KParams& p, uint32_t tacc, int c_begin, int gblk, float* area,
+inline __device__ __noinline__ void sk_store_partial(const KParams& p, uint32_t tacc, int c_begin, int gblk, float* area,
                                               int lane) {
 #pragma unroll 1
   for (int b = 0; b < p.mma_n / 64; ++b) {
@@ -285,7 +285,7 @@ __device__ __noinline__ void sk_store_partial(const KParams& p, uint32_t tacc, i
   }
 }
 // acc += the partials of clusters w0..w1 (in that order), block by block in TMEM
-__device__ __noinline__ void sk_add_partials(const KParams& p, uint32_t tacc, int c_begin, int gblk, int cta_rank,
+inline __device__ __noinline__ void sk_add_partials(const KParams& p, uint32_t tacc, int c_begin, int gblk, int cta_rank,
                                              int kcl, int ew, int w0, int w1, int lane) {
 #pragma unroll 1
   for (int b = 0; b < p.mma_n / 64; ++b) {
@@ -433,7 +433,7 @@ __device__ __forceinline__ float ldg_pinned(const void* base, long long i, int d
 // One thread waits, with the same bounded wait as the kernels, on an mbarrier that
 // nothing arrives on: the wait gives up after `limit_ns`, records kErrTimeout in
 // *err and the kernel returns, leaving the context usable.
-__global__ void fl_wait_selftest_kernel(int* err, unsigned long long limit_ns) {
+static __global__ void fl_wait_selftest_kernel(int* err, unsigned long long limit_ns) {
   __shared__ __align__(8) uint64_t bar;
   if (threadIdx.x != 0) return;
   const uint32_t b = smem_u32(&bar);

@@ -1,0 +1,292 @@
+// fl_rows.cu — entry points of the row kernels (fl_rows.cuh): dropout, dropout + residual +
+// LayerNorm, and its backward pass.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "fl_host.h"
+#include "fl_rows.cuh"
+
+using namespace fl;
+using namespace fl::host;
+
+namespace {
+
+constexpr int64_t kMaxCols = (1LL << 31) - 64;
+constexpr int64_t kMaxRows = (1LL << 31) - 1;
+
+fl_status drop_params(const char* who, const fl_dropout_desc* d, DropParams* out) {
+  memset(out, 0, sizeof(*out));
+  out->scale = 1.0f;
+  if (!d) return FL_OK;
+  if (!(d->p >= 0.0f && d->p < 1.0f)) return fail(FL_ERR_INVALID_ARG, "%s: the dropout probability must be in [0, 1)", who);
+  if (d->reserved != 0) return fail(FL_ERR_INVALID_ARG, "%s: reserved fields must be 0", who);
+  if (reinterpret_cast<uintptr_t>(d->offset_dev) % 8)
+    return fail(FL_ERR_ALIGNMENT, "%s: offset_dev must be 8-byte aligned", who);
+  out->k0 = (uint32_t)d->seed;
+  out->k1 = (uint32_t)(d->seed >> 32);
+  out->offset = d->offset;
+  out->offset_dev = d->offset_dev;
+  out->threshold = (uint32_t)((double)d->p * 4294967296.0);  // ⌊p·2^32⌋ (p < 1: below 2^32)
+  out->scale = (float)(1.0 / (1.0 - (double)d->p));
+  out->on = d->p > 0.0f;
+  return FL_OK;
+}
+
+// One matrix operand of an entry point: checked, its pitch defaulted, and whether each of its
+// rows starts on 16 bytes.
+struct Operand {
+  const char* name;
+  const void* p;
+  int64_t ld;
+  int dt;
+};
+fl_status check_operand(const char* who, const Operand& o, int64_t N, Mat* m, int* vec) {
+  const int es = esize(o.dt);
+  const int64_t ld = o.ld == 0 ? N : o.ld;
+  if (ld < N) return fail(FL_ERR_INVALID_ARG, "%s: leading dimension of %s < N", who, o.name);
+  if (reinterpret_cast<uintptr_t>(o.p) % es) return fail(FL_ERR_ALIGNMENT, "%s: %s is not aligned to its elements", who, o.name);
+  m->p = const_cast<void*>(o.p);
+  m->ld = ld;
+  m->dt = o.dt;
+  if (o.p && !(aligned16(o.p) && (ld * es) % 16 == 0)) *vec = 0;
+  return FL_OK;
+}
+fl_status check_param(const char* who, const char* name, const void* p, int dt, int* vec) {
+  if (reinterpret_cast<uintptr_t>(p) % esize(dt)) return fail(FL_ERR_ALIGNMENT, "%s: %s is not aligned to its elements", who, name);
+  if (p && !aligned16(p)) *vec = 0;
+  return FL_OK;
+}
+fl_status check_shape(const char* who, int64_t M, int64_t N) {
+  if (M < 0 || N < 0) return fail(FL_ERR_INVALID_ARG, "%s: negative size", who);
+  if (M > kMaxRows || N > kMaxCols) return fail(FL_ERR_INVALID_ARG, "%s: dimension too large", who);
+  return FL_OK;
+}
+fl_status num_sms(int* sms) {
+  int dev = 0;
+  FL_CUDA(cudaGetDevice(&dev));
+  FL_CUDA(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  return FL_OK;
+}
+
+// Kernel of one call: its launch bounds and the threads and vectors that hold a row.
+template <typename Args>
+struct RowKernel {
+  void (*fn)(Args);
+  int threads, vecs, block;  // threads 0: the kernel for rows of any length
+};
+template <int T, int V>
+RowKernel<DropLnArgs> ln_of() { return {fl_dropout_ln_kernel<T, V>, T, V, T < 128 ? 128 : T}; }
+template <int T, int V>
+RowKernel<DropLnBwdArgs> ln_bwd_of() { return {fl_dropout_ln_bwd_kernel<T, V>, T, V, T < 512 ? 512 : T}; }
+
+// Forward: two vectors a thread.
+RowKernel<DropLnArgs> ln_kernel(int64_t N) {
+  if (N <= 512) return ln_of<32, 2>();
+  if (N <= 1024) return ln_of<64, 2>();
+  if (N <= 2048) return ln_of<128, 2>();
+  if (N <= 4096) return ln_of<256, 2>();
+  if (N <= 8192) return ln_of<512, 2>();
+  if (N <= 16384) return ln_of<1024, 2>();
+  return {fl_dropout_ln_long_kernel, 0, 0, 1024};
+}
+// Backward: one vector a thread as far as a CTA goes, since the column sums stay in registers.
+RowKernel<DropLnBwdArgs> ln_bwd_kernel(int64_t N) {
+  if (N <= 256) return ln_bwd_of<32, 1>();
+  if (N <= 512) return ln_bwd_of<64, 1>();
+  if (N <= 1024) return ln_bwd_of<128, 1>();
+  if (N <= 2048) return ln_bwd_of<256, 1>();
+  if (N <= 4096) return ln_bwd_of<512, 1>();
+  if (N <= 8192) return ln_bwd_of<1024, 1>();
+  if (N <= 16384) return ln_bwd_of<1024, 2>();
+  return {fl_dropout_ln_bwd_long_kernel, 0, 0, 1024};
+}
+
+// Launch geometry of the backward pass: CTAs (each leaves one partial row of dγ and one of dβ)
+// and the pitch of those rows.  At most two CTAs per SM (one of 1024 threads), the residency the
+// kernel is built for: more would only add partial rows.
+struct BwdGeom {
+  RowKernel<DropLnBwdArgs> k;
+  int grid, ws_ld;
+  size_t bytes;
+};
+BwdGeom bwd_geom(int64_t M, int64_t N, int sms) {
+  BwdGeom g;
+  g.k = ln_bwd_kernel(N);
+  const int64_t ctas = cdiv(M, g.k.threads == 0 ? 1 : g.k.block / g.k.threads);
+  g.grid = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)sms * (g.k.block == 1024 ? 1 : 2)));
+  g.ws_ld = (int)(cdiv(N, 8) * 8);
+  g.bytes = (size_t)g.grid * 2 * (size_t)g.ws_ld * sizeof(float);
+  return g;
+}
+
+// The ring of rows ahead: two slots of `slot` bytes, or one where two do not fit, or none for
+// rows that are read in place.  A ring that takes a CTA above 48 KB with the kernel's own arrays
+// needs the kernel's opt-in.
+template <typename Args>
+fl_status ring_of(const RowKernel<Args>& k, size_t slot, Args* P, size_t* smem) {
+  constexpr size_t kMost = 200 * 1024;  // of the 227 KB of a CTA; the kernels' own arrays take at most 17 KB
+  P->ahead = kRowsAhead * slot <= kMost ? kRowsAhead : 1;
+  *smem = k.threads == 0 || !P->vec ? 0 : P->ahead * slot;
+  if (*smem > 24 * 1024)
+    FL_CUDA(cudaFuncSetAttribute((const void*)k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost));
+  return FL_OK;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ dropout
+extern "C" fl_status fl_dropout(const void* x, const void* residual, void* y, int64_t M, int64_t N, int64_t ld_x,
+                                int64_t ld_r, int64_t ld_y, int32_t x_dtype, int32_t y_dtype,
+                                const fl_dropout_desc* drop, void* stream_) {
+  clear_error();
+  const char* who = "fl_dropout";
+  if (!x || !y) return fail(FL_ERR_INVALID_ARG, "%s: null x or y", who);
+  fl_status st = check_shape(who, M, N);
+  if (st) return st;
+  if (!is_dtype(x_dtype) || !is_dtype(y_dtype)) return fail(FL_ERR_INVALID_ARG, "%s: unknown dtype", who);
+  DropoutArgs P{};
+  if ((st = drop_params(who, drop, &P.d))) return st;
+  P.vec = 1;
+  if ((st = check_operand(who, {"x", x, ld_x, x_dtype}, N, &P.x, &P.vec)) ||
+      (st = check_operand(who, {"residual", residual, ld_r, y_dtype}, N, &P.r, &P.vec)) ||
+      (st = check_operand(who, {"y", y, ld_y, y_dtype}, N, &P.y, &P.vec)))
+    return st;
+  if (M == 0 || N == 0) return FL_OK;
+  P.M = M;
+  P.N = (int)N;
+  P.nvec = (int)cdiv(N, 8);
+  int sms = 148;
+  if ((st = num_sms(&sms))) return st;
+  // two vectors a thread and trip; at most one resident wave of eight 256-thread CTAs per SM
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(cdiv(M * (int64_t)P.nvec, 512), (int64_t)sms * 8));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  const cudaError_t err = launch_pdl_b(fl_dropout_kernel, dim3((unsigned)grid), 256u, s, P);
+  if (err != cudaSuccess) return fail(FL_ERR_CUDA, "%s: kernel launch: %s", who, cudaGetErrorString(err));
+  return after_launch(s, who);
+}
+
+// ------------------------------------------------------------------ dropout, residual, LayerNorm
+extern "C" fl_status fl_dropout_layernorm(const void* x, const void* residual, const void* gamma, const void* beta,
+                                          void* sum, void* z, float* mean, float* rstd, int64_t M, int64_t N,
+                                          int64_t ld_x, int64_t ld_r, int64_t ld_sum, int64_t ld_z, int32_t x_dtype,
+                                          int32_t sum_dtype, int32_t z_dtype, int32_t param_dtype, float eps,
+                                          const fl_dropout_desc* drop, void* stream_) {
+  clear_error();
+  const char* who = "fl_dropout_layernorm";
+  if (!x || !z) return fail(FL_ERR_INVALID_ARG, "%s: null x or z", who);
+  if ((mean == nullptr) != (rstd == nullptr)) return fail(FL_ERR_INVALID_ARG, "%s: mean and rstd go together", who);
+  fl_status st = check_shape(who, M, N);
+  if (st) return st;
+  if (!is_dtype(x_dtype) || !is_dtype(sum_dtype) || !is_dtype(z_dtype) || !is_dtype(param_dtype))
+    return fail(FL_ERR_INVALID_ARG, "%s: unknown dtype", who);
+  if (!(eps >= 0.0f)) return fail(FL_ERR_INVALID_ARG, "%s: eps must be >= 0", who);
+  DropLnArgs P{};
+  if ((st = drop_params(who, drop, &P.d))) return st;
+  P.vec = 1;
+  if ((st = check_operand(who, {"x", x, ld_x, x_dtype}, N, &P.x, &P.vec)) ||
+      (st = check_operand(who, {"residual", residual, ld_r, sum_dtype}, N, &P.r, &P.vec)) ||
+      (st = check_operand(who, {"sum", sum, ld_sum, sum_dtype}, N, &P.s, &P.vec)) ||
+      (st = check_operand(who, {"z", z, ld_z, z_dtype}, N, &P.z, &P.vec)) ||
+      (st = check_param(who, "gamma", gamma, param_dtype, &P.vec)) ||
+      (st = check_param(who, "beta", beta, param_dtype, &P.vec)))
+    return st;
+  if (reinterpret_cast<uintptr_t>(mean) % 4 || reinterpret_cast<uintptr_t>(rstd) % 4)
+    return fail(FL_ERR_ALIGNMENT, "%s: mean or rstd is not 4-byte aligned", who);
+  if (M == 0 || N == 0) return FL_OK;
+  P.gamma = gamma;
+  P.beta = beta;
+  P.mean = mean;
+  P.rstd = rstd;
+  P.M = M;
+  P.N = (int)N;
+  P.param_dt = param_dtype;
+  P.eps = eps;
+  const RowKernel<DropLnArgs> k = ln_kernel(N);
+  const int64_t ctas = cdiv(M, k.threads == 0 ? 1 : k.block / k.threads);
+  size_t smem = 0;
+  if ((st = ring_of(k, operand_bytes(P.x, k.vecs, k.block) + operand_bytes(P.r, k.vecs, k.block), &P, &smem))) return st;
+  int sms = 148, per_sm = 0;
+  if ((st = num_sms(&sms))) return st;
+  // one resident wave of CTAs that walk the rows: their rows ahead are then always in flight
+  FL_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, (const void*)k.fn, k.block, smem));
+  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)std::max(1, per_sm) * sms);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  const cudaError_t err = launch_pdl_smem(k.fn, dim3(grid), (unsigned)k.block, smem, s, P);
+  if (err != cudaSuccess) return fail(FL_ERR_CUDA, "%s: kernel launch: %s", who, cudaGetErrorString(err));
+  return after_launch(s, who);
+}
+
+// ------------------------------------------------------------------ its backward pass
+extern "C" fl_status fl_layernorm_grad_workspace_size(int64_t M, int64_t N, size_t* bytes) {
+  clear_error();
+  const char* who = "fl_layernorm_grad_workspace_size";
+  if (!bytes) return fail(FL_ERR_INVALID_ARG, "%s: null pointer", who);
+  fl_status st = check_shape(who, M, N);
+  if (st) return st;
+  int sms = 148;
+  if ((st = num_sms(&sms))) return st;
+  *bytes = bwd_geom(M, N, sms).bytes;
+  return FL_OK;
+}
+
+extern "C" fl_status fl_dropout_layernorm_backward(
+    const void* dz, const void* dsum, const void* sum, const float* mean, const float* rstd, const void* gamma,
+    void* dres, void* dx, float* dgamma, float* dbeta, int64_t M, int64_t N, int64_t ld_dz, int64_t ld_dsum,
+    int64_t ld_sum, int64_t ld_dres, int64_t ld_dx, int32_t x_dtype, int32_t sum_dtype, int32_t z_dtype,
+    int32_t param_dtype, const fl_dropout_desc* drop, void* workspace, size_t workspace_bytes, void* stream_) {
+  clear_error();
+  const char* who = "fl_dropout_layernorm_backward";
+  if (!dz || !sum || !mean || !rstd) return fail(FL_ERR_INVALID_ARG, "%s: null dz, sum, mean or rstd", who);
+  if (!dres && !dx && !dgamma && !dbeta) return fail(FL_ERR_INVALID_ARG, "%s: no output", who);
+  fl_status st = check_shape(who, M, N);
+  if (st) return st;
+  if (!is_dtype(x_dtype) || !is_dtype(sum_dtype) || !is_dtype(z_dtype) || !is_dtype(param_dtype))
+    return fail(FL_ERR_INVALID_ARG, "%s: unknown dtype", who);
+  DropLnBwdArgs P{};
+  if ((st = drop_params(who, drop, &P.d))) return st;
+  P.vec = 1;
+  if ((st = check_operand(who, {"dz", dz, ld_dz, z_dtype}, N, &P.dz, &P.vec)) ||
+      (st = check_operand(who, {"dsum", dsum, ld_dsum, sum_dtype}, N, &P.ds_in, &P.vec)) ||
+      (st = check_operand(who, {"sum", sum, ld_sum, sum_dtype}, N, &P.s, &P.vec)) ||
+      (st = check_operand(who, {"dres", dres, ld_dres, sum_dtype}, N, &P.dres, &P.vec)) ||
+      (st = check_operand(who, {"dx", dx, ld_dx, x_dtype}, N, &P.dx, &P.vec)) ||
+      (st = check_param(who, "gamma", gamma, param_dtype, &P.vec)))
+    return st;
+  for (const void* p : {(const void*)mean, (const void*)rstd, (const void*)dgamma, (const void*)dbeta})
+    if (reinterpret_cast<uintptr_t>(p) % 4) return fail(FL_ERR_ALIGNMENT, "%s: an fp32 vector is not 4-byte aligned", who);
+  int sms = 148;
+  if ((st = num_sms(&sms))) return st;
+  const BwdGeom g = bwd_geom(M, N, sms);
+  const bool params = dgamma || dbeta;
+  if (params && (!workspace || workspace_bytes < g.bytes || !aligned16(workspace)))
+    return fail(FL_ERR_INVALID_ARG, "%s: dgamma and dbeta need a 16-byte aligned workspace of %zu bytes "
+                "(fl_layernorm_grad_workspace_size)", who, g.bytes);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  if (M == 0 || N == 0) {
+    for (float* q : {dgamma, dbeta})
+      if (q && N > 0) FL_CUDA(cudaMemsetAsync(q, 0, (size_t)N * sizeof(float), s));
+    return FL_OK;
+  }
+  P.mean = mean;
+  P.rstd = rstd;
+  P.gamma = gamma;
+  P.ws = params ? reinterpret_cast<float*>(workspace) : nullptr;
+  P.M = M;
+  P.N = (int)N;
+  P.ws_ld = g.ws_ld;
+  P.param_dt = param_dtype;
+  size_t smem = 0;
+  if ((st = ring_of(g.k, operand_bytes(P.dz, g.k.vecs, g.k.block) + operand_bytes(P.s, g.k.vecs, g.k.block) +
+                             operand_bytes(P.ds_in, g.k.vecs, g.k.block), &P, &smem)))
+    return st;
+  cudaError_t err = launch_pdl_smem(g.k.fn, dim3((unsigned)g.grid), (unsigned)g.k.block, smem, s, P);
+  if (err != cudaSuccess) return fail(FL_ERR_CUDA, "%s: kernel launch: %s", who, cudaGetErrorString(err));
+  if (params) {
+    if ((st = after_launch(s, who))) return st;
+    err = launch_pdl_b(fl_ln_wgrad_kernel, dim3((unsigned)cdiv(N, 32), 2u), 1024u, s, (const float*)P.ws, dgamma, dbeta,
+                       P.N, P.ws_ld, g.grid);
+    if (err != cudaSuccess) return fail(FL_ERR_CUDA, "%s: reduction kernel launch: %s", who, cudaGetErrorString(err));
+  }
+  return after_launch(s, who);
+}

@@ -211,6 +211,76 @@ fl_status fl_layernorm(const void* x, const void* gamma, const void* beta, void*
                        int64_t ld_x, int64_t ld_z, int32_t x_dtype, int32_t z_dtype, int32_t param_dtype,
                        float eps, void* stream);
 
+/* Dropout from a counter-based generator: no mask is stored, the backward pass draws the
+ * same decisions again (no counterpart on the pages; the step between a sublayer's output
+ * projection and its residual add in training).  The decision of element (m, n) of an
+ * M x N matrix comes from word n mod 4 of Philox4x32-10 with key `seed` and counter
+ * (m*ceil(N/4) + n/4, offset), both 64 bits with the low half first: the element is dropped
+ * when the word is below floor(p*2^32), else multiplied by 1/(1-p).  It depends on M x N
+ * indices only, not on pitches, types or the launch.  A dropped element gives exactly 0,
+ * whatever x holds there (infinities and NaN included).  Calls with the same seed and
+ * different offsets draw independent numbers. */
+typedef struct {
+  float p;                    /* probability of dropping an element, in [0, 1); 0: none dropped */
+  int32_t reserved;           /* must be 0 */
+  uint64_t seed, offset;
+  const uint64_t* offset_dev; /* device pointer, 8-byte aligned, or null: added to offset (modulo
+                                 2^64) when the kernel runs, so that a captured graph draws new
+                                 numbers at each replay if the caller advances it in between */
+} fl_dropout_desc;
+
+/* y = residual + D(x), D the dropout above (drop null: D(x) = x).  Forward and backward in
+ * one: the gradient of x is D of y's gradient with the same seed and offset, and the
+ * residual's gradient is y's gradient itself.
+ *   x [M, ld_x] of x_dtype; residual (or null) [M, ld_r] and y [M, ld_y] of y_dtype; ld 0 = N.
+ *   y may be x's or the residual's own buffer with the same type and pitch.
+ * Any alignment of the elements is accepted; rows that all start on 16 bytes run fastest.
+ * Errors: FL_ERR_INVALID_ARG (null x or y, size, ld < N, dtype, p outside [0, 1)),
+ * FL_ERR_ALIGNMENT, FL_ERR_CUDA. */
+fl_status fl_dropout(const void* x, const void* residual, void* y, int64_t M, int64_t N, int64_t ld_x, int64_t ld_r,
+                     int64_t ld_y, int32_t x_dtype, int32_t y_dtype, const fl_dropout_desc* drop, void* stream);
+
+/* The end of a sublayer in training, in one kernel ([mhc] §3.2 fuses the residual add and
+ * the row's normalisation):
+ *   s = residual + D(x),  z = (s − μ_m)·rstd_m·gamma + beta,  rstd_m = 1/√(σ²_m + eps),
+ * μ_m and σ²_m the mean and the population variance of row m of s, in fp32, of s before it is
+ * rounded to its type.
+ *   x [M, ld_x] of x_dtype; residual (null: none) and sum (the stored s; null: not stored)
+ *   [M, ld_r], [M, ld_sum] of sum_dtype; z [M, ld_z] of z_dtype; gamma, beta [N] of
+ *   param_dtype (null gamma = 1, null beta = 0); mean, rstd [M] fp32, both or neither: what
+ *   the backward pass reads.  drop null: no dropout.  ld 0 = N.
+ *   sum and z may each be x's or the residual's own buffer with the same type and pitch (not
+ *   both the same one).
+ * Errors: as fl_layernorm, and FL_ERR_INVALID_ARG for p outside [0, 1). */
+fl_status fl_dropout_layernorm(const void* x, const void* residual, const void* gamma, const void* beta, void* sum,
+                               void* z, float* mean, float* rstd, int64_t M, int64_t N, int64_t ld_x, int64_t ld_r,
+                               int64_t ld_sum, int64_t ld_z, int32_t x_dtype, int32_t sum_dtype, int32_t z_dtype,
+                               int32_t param_dtype, float eps, const fl_dropout_desc* drop, void* stream);
+
+/* Its backward pass.  With u = (s − μ)·rstd and g = dz·gamma:
+ *   ds = rstd·(g − mean_n(g) − u·mean_n(g·u)) + dsum,  dres = ds,  dx = D(ds),
+ *   dgamma[n] = Σ_m dz·u,  dbeta[n] = Σ_m dz  (fp32, summed in a fixed order).
+ * dx is D of ds before ds is rounded to its type.
+ *   dz [M, ld_dz] of z_dtype; dsum [M, ld_dsum] of sum_dtype, the gradient that reaches s by
+ *   the residual stream of a pre-norm block, or null; sum [M, ld_sum] of sum_dtype, mean, rstd
+ *   [M]: from the forward pass (for a plain LayerNorm, sum is its input x); gamma as there.
+ *   dres [M, ld_dres] of sum_dtype, dx [M, ld_dx] of x_dtype, dgamma, dbeta [N] fp32: each may
+ *   be null (not wanted), not all.  dres and dx may each be dz's, dsum's or sum's own buffer with
+ *   the same type and pitch (not both the same one).  M = 0 gives dgamma = dbeta = 0.
+ *   workspace: needed for dgamma and dbeta; fl_layernorm_grad_workspace_size bytes (for the
+ *   current device), 16-byte aligned, owned by the caller, no initial contents needed.  Calls
+ *   that overlap on the GPU must not share it.
+ * Errors: FL_ERR_INVALID_ARG (null operand, no output, size, ld < N, dtype, p, workspace),
+ * FL_ERR_ALIGNMENT, FL_ERR_CUDA. */
+fl_status fl_layernorm_grad_workspace_size(int64_t M, int64_t N, size_t* bytes);
+fl_status fl_dropout_layernorm_backward(const void* dz, const void* dsum, const void* sum, const float* mean,
+                                        const float* rstd, const void* gamma, void* dres, void* dx, float* dgamma,
+                                        float* dbeta, int64_t M, int64_t N, int64_t ld_dz, int64_t ld_dsum,
+                                        int64_t ld_sum, int64_t ld_dres, int64_t ld_dx, int32_t x_dtype,
+                                        int32_t sum_dtype, int32_t z_dtype, int32_t param_dtype,
+                                        const fl_dropout_desc* drop, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
 /* Synchronise `stream` and read the plan's device error word.  Returns
  * FL_ERR_TIMEOUT if a bounded wait inside a kernel of this plan gave up
  * (the error word is then cleared), FL_ERR_CUDA on a CUDA error, else FL_OK. */
