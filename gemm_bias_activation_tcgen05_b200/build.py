@@ -22,7 +22,8 @@ OBJ_DIR = os.path.join(HERE, "_build")
 _GEMM = ["fl_gemm.cuh", "fl_ptx.cuh", "fl_host.h"]
 # each translation unit and the headers it includes
 UNITS = {
-    "fl_api.cu": ["fl_elementwise.cuh", *_GEMM],
+    "fl_api.cu": ["fl_elementwise.cuh", "fl_plan.h", *_GEMM],
+    "fl_pair.cu": ["fl_pair.cuh", "fl_plan.h", *_GEMM],
     "fl_rows.cu": ["fl_rows.cuh", *_GEMM],
 }
 HEADER = os.path.join(ROOT, "include", "fused_linear.h")

@@ -21,6 +21,7 @@
 #include "fl_elementwise.cuh"
 #include "fl_gemm.cuh"
 #include "fl_host.h"
+#include "fl_plan.h"
 
 using namespace fl;
 using namespace fl::host;
@@ -180,46 +181,6 @@ static const void* pick_kernel(int act, int out, bool swap) {
 }
 
 // ------------------------------------------------------------------ plan
-// Tensor maps and kernel parameters of the last launch of one call site: a
-// repeat call with the same operand pointers launches without re-encoding.
-struct LaunchCache {
-  bool valid = false;
-  const void* key[8] = {};
-  CUtensorMap tmA, tmB, tmB2, tmOut;
-  KParams k;
-};
-
-struct fl_plan_s {
-  int64_t M, N, K;
-  int dtype, compute;
-  fl_epilogue_desc epi;
-  int act;
-  bool has_bias, has_aux;
-  int device, num_sms, max_smem;
-  // configuration
-  bool swap;
-  bool pair;  // two CTAs share one 256-row UMMA tile (cluster of 2)
-  int k_atoms;  // 128-byte K atoms per pipeline stage
-  int mma_n, out_tile_n, split_k, stages, grid, smem;
-  int tiles_a, tiles_b, num_kb;
-  // stream-K (16-bit CTA pairs): the last sk_tiles tiles are split along K over
-  // sk_clusters pairs; no_sk keeps the data-parallel schedule
-  bool no_sk;
-  int sk_tiles, sk_clusters;
-  float* d_skws;  // partial accumulators, sk_ws_bytes()
-  int* d_skflags;
-  size_t skws_bytes, skflags_bytes;
-  const void* kernel;
-  int* d_err;
-  // unfused twin
-  void* d_tmp;
-  int64_t tmp_ld;
-  size_t tmp_bytes;
-  int launches;
-  uint64_t wait_limit_ns;
-  LaunchCache cache_fused, cache_unfused;
-};
-
 static int act_of(int kind) {
   switch (kind) {
     case FL_EPI_RELU_BIAS:
@@ -488,7 +449,7 @@ static fl_status plan_host_part(fl_plan_s** out, int64_t M, int64_t N, int64_t K
                                            (long long)M, (long long)N, (long long)K);
   if (M > (1LL << 31) - 256 || N > (1LL << 30) || K > (1LL << 31) - 256)
     return fail(FL_ERR_INVALID_ARG, "fl_plan: dimension too large");
-  if (epi->kind < FL_EPI_NONE || epi->kind > FL_EPI_GELU_SIGMOID_BIAS)
+  if (epi->kind < FL_EPI_NONE || epi->kind > FL_EPI_WGRAD)
     return fail(FL_ERR_INVALID_ARG, "fl_plan: unknown epilogue kind %d", epi->kind);
   for (int i = 0; i < 2; ++i)
     if (epi->reserved[i] != 0) return fail(FL_ERR_INVALID_ARG, "fl_plan: reserved fields must be 0");
@@ -504,7 +465,8 @@ static fl_status plan_host_part(fl_plan_s** out, int64_t M, int64_t N, int64_t K
     return fail(FL_ERR_UNSUPPORTED, "fl_plan: fp32 operands take a K-contiguous W and no GeGLU");
   if (epi->out_dtype < FL_F16 || epi->out_dtype > FL_F32)
     return fail(FL_ERR_INVALID_ARG, "fl_plan: unknown out_dtype %d", epi->out_dtype);
-  const bool has_bias = epi->kind != FL_EPI_NONE && epi->kind != FL_EPI_GEGLU_TANH;
+  const bool pair = pair_kind(epi->kind);
+  const bool has_bias = epi->kind != FL_EPI_NONE && epi->kind != FL_EPI_GEGLU_TANH && !pair;
   if (has_bias && (epi->bias_dtype < FL_F16 || epi->bias_dtype > FL_F32))
     return fail(FL_ERR_INVALID_ARG, "fl_plan: unknown bias_dtype %d", epi->bias_dtype);
   if (epi->has_residual && (epi->residual_dtype < FL_F16 || epi->residual_dtype > FL_F32))
@@ -520,6 +482,10 @@ static fl_status plan_host_part(fl_plan_s** out, int64_t M, int64_t N, int64_t K
     return fail(FL_ERR_UNSUPPORTED, "fl_plan: the unfused twin has no GELU_AUX_BIAS step");
   if (epi->lda < 0 || epi->ldb < 0 || epi->ldo < 0 || epi->ldr < 0)
     return fail(FL_ERR_INVALID_ARG, "fl_plan: negative leading dimension");
+  if (pair) {
+    const fl_status st = pair_check("fl_plan", M, N, K, dtype, epi);
+    if (st) return st;
+  }
 
   fl_plan_s* p = new (std::nothrow) fl_plan_s();
   if (!p) return fail(FL_ERR_OOM, "fl_plan: host allocation failed");
@@ -527,14 +493,16 @@ static fl_status plan_host_part(fl_plan_s** out, int64_t M, int64_t N, int64_t K
   if (p->epi.scale == 0.0f) p->epi.scale = 1.0f;
   p->act = act_of(epi->kind);
   p->has_bias = has_bias;
-  p->has_aux = epi->kind == FL_EPI_RELU_AUX_BIAS || epi->kind == FL_EPI_GELU_AUX_BIAS;
+  p->has_aux = epi->kind == FL_EPI_RELU_AUX_BIAS || epi->kind == FL_EPI_GELU_AUX_BIAS || glu_aux_kind(epi->kind) ||
+               dglu_kind(epi->kind);
   // leading dimensions default to packed
-  const int64_t a_cols = K, b_cols = epi->b_major ? N : K;
+  const int64_t a_cols = epi->kind == FL_EPI_WGRAD ? M : K, b_cols = epi->b_major ? N : K;
+  const int64_t o_cols = dglu_kind(epi->kind) ? 2 * N : N;
   if (p->epi.lda == 0) p->epi.lda = a_cols;
   if (p->epi.ldb == 0) p->epi.ldb = b_cols;
-  if (p->epi.ldo == 0) p->epi.ldo = N;
+  if (p->epi.ldo == 0) p->epi.ldo = o_cols;
   if (p->epi.ldr == 0) p->epi.ldr = N;
-  if (p->epi.lda < a_cols || p->epi.ldb < b_cols || p->epi.ldo < N || (epi->has_residual && p->epi.ldr < N)) {
+  if (p->epi.lda < a_cols || p->epi.ldb < b_cols || p->epi.ldo < o_cols || (epi->has_residual && p->epi.ldr < N)) {
     delete p;
     return fail(FL_ERR_INVALID_ARG, "fl_plan: leading dimension smaller than the row length");
   }
@@ -574,6 +542,24 @@ extern "C" fl_status fl_plan(fl_plan_t* out, int64_t M, int64_t N, int64_t K, in
   p->max_smem = (int)prop.sharedMemPerBlockOptin;
   fl_status st = get_encode();
   if (st != FL_OK) { delete p; return st; }
+  if (pair_kind(epi->kind)) {
+    if ((st = pair_config(p, false)) || (st = pair_prepare(p))) { delete p; return st; }
+    const size_t ws = pair_workspace_bytes(p);
+    if (cudaMalloc(&p->d_err, sizeof(int)) != cudaSuccess ||
+        (ws > 0 && cudaMalloc(&p->d_skws, ws) != cudaSuccess)) {
+      (void)cudaGetLastError();
+      fl_free(p);
+      return fail(FL_ERR_OOM, "fl_plan: cudaMalloc(error word, workspace of %zu bytes)", ws);
+    }
+    p->skws_bytes = ws;
+    if (cudaMemset(p->d_err, 0, sizeof(int)) != cudaSuccess) {
+      fl_free(p);
+      return fail(FL_ERR_CUDA, "fl_plan: cudaMemset(error word)");
+    }
+    p->wait_limit_ns = g_wait_limit_ns;
+    *out = p;
+    return FL_OK;
+  }
 
   choose_config(p);
   const int b_boxes = b_boxes_of(p, p->epi.kind == FL_EPI_GEGLU_TANH);
@@ -671,6 +657,12 @@ extern "C" fl_status fl_plan_preview(int64_t M, int64_t N, int64_t K, int32_t dt
   if (st != FL_OK) return st;
   p->num_sms = num_sms;
   p->max_smem = max_smem_per_block;
+  if (pair_kind(p->epi.kind)) {
+    fl_status r = pair_config(p, false);
+    if (r == FL_OK) r = fl_get_plan_info(p, info);
+    delete p;
+    return r;
+  }
   choose_config(p);
   const int b_boxes = b_boxes_of(p, p->epi.kind == FL_EPI_GEGLU_TANH);
   const Layout L = layout_for(p, p->mma_n, b_boxes, p->max_smem);
@@ -955,10 +947,10 @@ extern "C" fl_status fl_execute(fl_plan_t p, const void* A, const void* W, const
     return fail(FL_ERR_INVALID_ARG, "fl_execute: A, W (when K > 0) and out are required");
   if (p->has_bias && !bias) return fail(FL_ERR_INVALID_ARG, "fl_execute: this epilogue needs a bias");
   if (!p->has_bias && bias) return fail(FL_ERR_INVALID_ARG, "fl_execute: this epilogue takes no bias");
-  if (p->has_aux && !aux) return fail(FL_ERR_INVALID_ARG, "fl_execute: RELU_AUX_BIAS / GELU_AUX_BIAS need the aux buffer");
-  if (!p->has_aux && aux) return fail(FL_ERR_INVALID_ARG, "fl_execute: only the AUX epilogues write an aux buffer");
-  if (aux && p->epi.kind == FL_EPI_GELU_AUX_BIAS && !aligned16(aux))
-    return fail(FL_ERR_ALIGNMENT, "fl_execute: the GELU_AUX_BIAS pre-activation buffer must be 16-byte aligned");
+  if (p->has_aux && !aux) return fail(FL_ERR_INVALID_ARG, "fl_execute: this epilogue needs the aux buffer");
+  if (!p->has_aux && aux) return fail(FL_ERR_INVALID_ARG, "fl_execute: this epilogue takes no aux buffer");
+  if (aux && p->epi.kind != FL_EPI_RELU_AUX_BIAS && !aligned16(aux))
+    return fail(FL_ERR_ALIGNMENT, "fl_execute: the pre-activation buffer must be 16-byte aligned");
   if (p->epi.has_residual && !residual) return fail(FL_ERR_INVALID_ARG, "fl_execute: has_residual needs a residual");
   if (!p->epi.has_residual && residual) return fail(FL_ERR_INVALID_ARG, "fl_execute: residual given but not planned");
   if ((p->K > 0 && (!aligned16(A) || !aligned16(W))) || !aligned16(out) || (residual && !aligned16(residual)))
@@ -972,6 +964,7 @@ extern "C" fl_status fl_execute(fl_plan_t p, const void* A, const void* W, const
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const fl_epilogue_desc& e = p->epi;
   const bool geglu = e.kind == FL_EPI_GEGLU_TANH;
+  if (pair_kind(e.kind)) return pair_execute(p, A, W, aux_, residual, out, stream);
 
   if (!e.unfused) {
     GemmArgs g{A, W, out, e.out_dtype, e.ldo, p->act, bias, residual, aux, e.scale, p->N, geglu};
@@ -1380,6 +1373,32 @@ static fl_status noalloc_scratch(int dev, unsigned char** out) {
   return FL_OK;
 }
 
+// The kinds of fl_pair.cuh: the same configuration as fl_plan's, but with no K splits, which need
+// a workspace.
+static fl_status noalloc_pair(int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t compute,
+                              const fl_epilogue_desc* epi, const void* A, const void* W, const void* bias, void* aux,
+                              const void* residual, void* out, void* stream_) {
+  const char* who = "fl_execute_noalloc";
+  fl_plan_s* made = nullptr;
+  fl_status st = plan_host_part(&made, M, N, K, dtype, compute, epi);
+  if (st != FL_OK) return st;
+  fl_plan_s p = *made;
+  delete made;
+  if (cudaGetDevice(&p.device) != cudaSuccess) return fail(FL_ERR_DEVICE, "%s: no CUDA device", who);
+  int major = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, p.device) != cudaSuccess || major != 10)
+    return fail(FL_ERR_DEVICE, "%s: needs an sm_100 (B200-class) GPU", who);
+  FL_CUDA(cudaDeviceGetAttribute(&p.num_sms, cudaDevAttrMultiProcessorCount, p.device));
+  FL_CUDA(cudaDeviceGetAttribute(&p.max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, p.device));
+  if ((st = get_encode()) || (st = pair_config(&p, true)) || (st = pair_prepare(&p))) return st;
+  p.wait_limit_ns = g_wait_limit_ns;
+  unsigned char* scratch = nullptr;
+  if ((st = noalloc_scratch(p.device, &scratch))) return st;
+  p.d_err = reinterpret_cast<int*>(scratch);
+  FL_CUDA(cudaMemsetAsync(p.d_err, 0, sizeof(int), reinterpret_cast<cudaStream_t>(stream_)));
+  return fl_execute(&p, A, W, bias, aux, residual, out, stream_);
+}
+
 extern "C" fl_status fl_execute_noalloc(int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t compute,
                                         const fl_epilogue_desc* epi, const void* A, const void* W,
                                         const void* bias, void* aux_, const void* residual, void* out,
@@ -1388,6 +1407,7 @@ extern "C" fl_status fl_execute_noalloc(int64_t M, int64_t N, int64_t K, int32_t
   uint32_t* aux = static_cast<uint32_t*>(aux_);
   const char* who = "fl_execute_noalloc";
   if (!epi) return fail(FL_ERR_INVALID_ARG, "%s: null epilogue descriptor", who);
+  if (pair_kind(epi->kind)) return noalloc_pair(M, N, K, dtype, compute, epi, A, W, bias, aux_, residual, out, stream_);
   if (M < 1 || N < 1 || K < 0) return fail(FL_ERR_INVALID_ARG, "%s: need M>=1, N>=1, K>=0", who);
   if (M > (1LL << 31) - 256 || N > (1LL << 30) || K > (1LL << 31) - 256)
     return fail(FL_ERR_INVALID_ARG, "%s: dimension too large", who);

@@ -1,0 +1,255 @@
+// fl_pair.cu — configuration and launch of the gated linear units, their backward and the weight
+// gradient (kernels in fl_pair.cuh).
+#include <algorithm>
+#include <cstring>
+
+#include "fl_host.h"
+#include "fl_pair.cuh"
+#include "fl_plan.h"
+
+using namespace fl;
+using namespace fl::host;
+
+namespace {
+
+using PairFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, KParams);
+
+int epi_of(int kind) {
+  switch (kind) {
+    case FL_EPI_SWIGLU: return EPI_GLU;
+    case FL_EPI_GEGLU_TANH_AUX:
+    case FL_EPI_SWIGLU_AUX: return EPI_GLU_AUX;
+    case FL_EPI_DGEGLU_TANH:
+    case FL_EPI_DSWIGLU: return EPI_DGLU;
+    default: return EPI_GRAD;
+  }
+}
+bool is_geglu(int kind) { return kind == FL_EPI_GEGLU_TANH_AUX || kind == FL_EPI_DGEGLU_TANH; }
+
+template <int EPI, int ACT>
+PairFn by_out(int out) {
+  return out == FL_BF16 ? &fl_pair_tcgen05<EPI, ACT, DT_BF16> : &fl_pair_tcgen05<EPI, ACT, DT_F16>;
+}
+// `out`: the type that the kernel itself writes (fp32 partial tiles with K splits)
+PairFn pair_kernel(int kind, int out) {
+  switch (kind) {
+    case FL_EPI_SWIGLU: return by_out<EPI_GLU, GATE_SWIGLU>(out);
+    case FL_EPI_GEGLU_TANH_AUX: return by_out<EPI_GLU_AUX, GATE_GEGLU_TANH>(out);
+    case FL_EPI_SWIGLU_AUX: return by_out<EPI_GLU_AUX, GATE_SWIGLU>(out);
+    case FL_EPI_DGEGLU_TANH: return by_out<EPI_DGLU, GATE_GEGLU_TANH>(out);
+    case FL_EPI_DSWIGLU: return by_out<EPI_DGLU, GATE_SWIGLU>(out);
+    default: return out == FL_F32 ? &fl_pair_tcgen05<EPI_GRAD, GATE_SWIGLU, DT_F32> : by_out<EPI_GRAD, GATE_SWIGLU>(out);
+  }
+}
+int kernel_out(const fl_plan_s* p) { return p->split_k > 1 ? FL_F32 : p->epi.out_dtype; }
+
+// Rows and pitch of one split's partial tiles in the workspace: whole 256-row tiles, and rows of
+// whole 32-column blocks.
+int64_t split_rows(const fl_plan_s* p) { return 256LL * p->tiles_a; }
+int64_t ws_ld(const fl_plan_s* p) { return cdiv(p->N, 32) * 32; }
+
+}  // namespace
+
+fl_status fl::host::pair_check(const char* who, int64_t M, int64_t N, int64_t K, int32_t dtype, const fl_epilogue_desc* e) {
+  const bool wgrad = e->kind == FL_EPI_WGRAD;
+  const bool need_b_major = wgrad || dglu_kind(e->kind);
+  if (dtype == FL_F32) return fail(FL_ERR_UNSUPPORTED, "%s: this kind takes f16/bf16 operands", who);
+  if (e->unfused) return fail(FL_ERR_UNSUPPORTED, "%s: this kind has no unfused twin", who);
+  if (e->schedule != FL_SCHED_AUTO) return fail(FL_ERR_UNSUPPORTED, "%s: this kind chooses its own schedule", who);
+  if ((e->b_major != 0) != need_b_major)
+    return fail(FL_ERR_UNSUPPORTED, need_b_major ? "%s: this kind takes W stored [K,N] (b_major 1)"
+                                                 : "%s: this kind takes the stacked [2N,K] weight (b_major 0)", who);
+  if (!wgrad && e->out_dtype == FL_F32) return fail(FL_ERR_UNSUPPORTED, "%s: this kind writes f16/bf16", who);
+  if (!wgrad && (e->has_residual || (e->scale != 0.0f && e->scale != 1.0f)))
+    return fail(FL_ERR_UNSUPPORTED, "%s: this kind has no residual and no scale", who);
+  if ((glu_aux_kind(e->kind) || dglu_kind(e->kind)) && N % 8 != 0)
+    return fail(FL_ERR_ALIGNMENT, "%s: the halves of a [M,2N] buffer start on 16 bytes only when N is a multiple of 8", who);
+  (void)M;
+  (void)K;
+  return FL_OK;
+}
+
+// Tile width, K splits, stages and grid.
+//  * A tile is 256 rows by 256 accumulator columns (GLU: 128 gate and 128 up), or by 128 where
+//    narrower tiles take fewer or better filled rounds of the GPU's pairs.
+//  * GRAD: a gradient of few tiles would leave most pairs idle while each walks all tokens, so K is
+//    cut into S splits; S minimises the estimated time below.
+fl_status fl::host::pair_config(fl_plan_s* p, bool no_workspace) {
+  const int epi = epi_of(p->epi.kind);
+  const bool glu = epi == EPI_GLU || epi == EPI_GLU_AUX;
+  const int64_t P = std::max(1, p->num_sms / 2);
+  p->swap = false;
+  p->pair = true;
+  p->k_atoms = 1;
+  p->num_kb = (int)cdiv(p->K, kPairBk);
+  double best = 1e300;
+  for (int width : {256, 128}) {
+    const int64_t tiles = cdiv(p->M, 256) * cdiv(p->N, glu ? width / 2 : width);
+    // microseconds of a 64-deep K block, and of what a tile adds outside its K loop
+    const double block_us = width == 256 ? 0.29 : 0.19, tile_us = width == 256 ? 2.0 : 1.5;
+    const int most = epi == EPI_GRAD && !no_workspace ? std::min(p->num_kb, 32) : 1;
+    for (int S = 1; S <= std::max(1, most); ++S) {
+      if (tiles * S >= (1LL << 24)) break;  // the tile raster's range
+      double us = (double)cdiv(tiles * S, P) * ((double)cdiv(p->num_kb, S) * block_us + tile_us);
+      // the partial tiles are written and read once more (mostly through L2), by one more launch
+      if (S > 1) us += 3.0 + (double)S * 8.0 * (double)p->M * (double)p->N / 8e6;
+      if (us < best) {
+        best = us;
+        p->mma_n = width;
+        p->split_k = S;
+      }
+    }
+  }
+  if (best >= 1e300) return fail(FL_ERR_INVALID_ARG, "fl_plan: dimension too large");
+  p->out_tile_n = glu ? p->mma_n / 2 : p->mma_n;
+  p->tiles_a = (int)cdiv(p->M, 256);
+  p->tiles_b = (int)cdiv(p->N, p->out_tile_n);
+  const uint32_t staging = 8u * pair_warp_staging(epi, kernel_out(p));
+  const uint32_t stage = kPairABytes + (uint32_t)(p->mma_n / 2) * 128u;
+  const int64_t room = (int64_t)p->max_smem - 1024 - staging - kPairBarBytes;
+  p->stages = (int)std::min<int64_t>(12, std::max<int64_t>(0, room) / stage);
+  if (p->stages < 2) return fail(FL_ERR_UNSUPPORTED, "fl_plan: shared memory too small");
+  p->smem = (int)(1024 + (uint32_t)p->stages * stage + staging + kPairBarBytes);
+  p->grid = (int)(2 * std::min<int64_t>((int64_t)p->tiles_a * p->tiles_b * p->split_k, P));
+  p->kernel = reinterpret_cast<const void*>(pair_kernel(p->epi.kind, kernel_out(p)));
+  p->launches = p->split_k > 1 ? 2 : 1;
+  return FL_OK;
+}
+
+fl_status fl::host::pair_prepare(const fl_plan_s* p) {
+  FL_CUDA(cudaFuncSetAttribute(p->kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p->max_smem));
+  return FL_OK;
+}
+
+size_t fl::host::pair_workspace_bytes(const fl_plan_s* p) {
+  return p->split_k > 1 ? (size_t)p->split_k * (size_t)split_rows(p) * (size_t)ws_ld(p) * sizeof(float) : 0;
+}
+
+fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, void* aux, const void* residual, void* out,
+                                 cudaStream_t stream) {
+  const fl_epilogue_desc& e = p->epi;
+  const int epi = epi_of(e.kind);
+  const bool glu = epi == EPI_GLU || epi == EPI_GLU_AUX;
+  const bool split = p->split_k > 1;
+  const int kout = kernel_out(p);
+  const uint64_t es = 2, eo = (uint64_t)esize(e.out_dtype);
+  const uint64_t M = (uint64_t)p->M, N = (uint64_t)p->N, K = (uint64_t)p->K;
+
+  KParams k{};
+  k.M = (int)p->M;
+  k.N = split ? (int)ws_ld(p) : (int)p->N;
+  k.K = (int)p->K;
+  k.tiles_a = p->tiles_a;
+  k.tiles_b = p->tiles_b;
+  k.num_kb = p->num_kb;
+  k.split_k = p->split_k;
+  k.num_stages = p->stages;
+  k.mma_n = p->mma_n;
+  k.out_tile_n = p->out_tile_n;
+  k.b_boxes = p->mma_n / 128;  // 64-column boxes of this CTA's half of an MN-major B
+  k.stage_bytes = k.stage_stride = kPairABytes + (uint32_t)(p->mma_n / 2) * 128u;
+  const uint32_t fmt = p->dtype == FL_BF16 ? 1u : 0u;
+  k.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(pair_a_mn(epi) ? 1 : 0) << 15) |
+            ((uint32_t)(pair_b_mn(epi) ? 1 : 0) << 16) | ((uint32_t)(p->mma_n >> 3) << 17) | ((256u >> 4) << 24);
+  k.tmem_cols = (uint32_t)(2 * p->mma_n);
+  k.staging_off = (uint32_t)p->stages * k.stage_stride;
+  k.bar_off = k.staging_off + 8u * pair_warp_staging(epi, kout);
+  k.residual = split ? nullptr : residual;
+  k.ldr = e.ldr;
+  k.res_dtype = e.residual_dtype;
+  k.out = out;
+  k.ldo = e.ldo;
+  k.scale = split ? 1.0f : e.scale;
+  k.err = p->d_err;
+  k.wait_limit_ns = p->wait_limit_ns;
+  const int units = p->tiles_a * p->tiles_b * p->split_k, pairs = p->grid / 2;
+  k.dp_q = units / pairs;
+  k.dp_r = units % pairs;
+  k.inv_group = 1.0f / (float)(8 * p->tiles_b);
+  k.split_rows = split ? (int)split_rows(p) : 0;
+
+  CUtensorMap mA, mB, mB2, m0, m1, m2, m3;
+  for (CUtensorMap* m : {&mA, &mB, &mB2, &m0, &m1, &m2, &m3}) memset(m, 0, sizeof(*m));
+  fl_status st = FL_OK;
+  if (K > 0) {
+    st = pair_a_mn(epi) ? make_map(&mA, A, p->dtype, M, K, (uint64_t)e.lda * es, 64, kPairBk)
+                        : make_map(&mA, A, p->dtype, K, M, (uint64_t)e.lda * es, 64, 128);
+    if (st) return st;
+    if (pair_b_mn(epi)) {
+      st = make_map(&mB, W, p->dtype, N, K, (uint64_t)e.ldb * es, 64, kPairBk);
+    } else {
+      st = make_map(&mB, W, p->dtype, K, N, (uint64_t)e.ldb * es, 64, (uint32_t)p->out_tile_n);
+      if (st) return st;
+      const char* up = static_cast<const char*>(W) + N * (uint64_t)e.ldb * es;
+      st = make_map(&mB2, up, p->dtype, K, N, (uint64_t)e.ldb * es, 64, (uint32_t)p->out_tile_n);
+    }
+    if (st) return st;
+  }
+  // the epilogue's tiles: 32 rows x 32 columns
+  auto tile = [&](CUtensorMap* m, const void* base, int dt, uint64_t cols, uint64_t rows, uint64_t pitch) {
+    return make_map(m, base, dt, cols, rows, pitch, 32, 32, dt != FL_F32);
+  };
+  if (epi == EPI_DGLU) {
+    const char* g = static_cast<const char*>(aux);
+    char* dg = static_cast<char*>(out);
+    if ((st = tile(&m0, g, e.out_dtype, N, M, 2 * N * eo)) || (st = tile(&m1, g + N * eo, e.out_dtype, N, M, 2 * N * eo)) ||
+        (st = tile(&m2, dg, e.out_dtype, N, M, (uint64_t)e.ldo * eo)) ||
+        (st = tile(&m3, dg + N * eo, e.out_dtype, N, M, (uint64_t)e.ldo * eo)))
+      return st;
+    k.n_tma = (int)N;
+  } else if (split) {
+    k.n_tma = k.N;
+    st = tile(&m0, p->d_skws, FL_F32, (uint64_t)k.N, (uint64_t)p->split_k * (uint64_t)split_rows(p), (uint64_t)k.N * 4);
+    if (st) return st;
+  } else {
+    // whole 16-byte granules of a row go out by TMA, the ragged remainder by plain stores
+    k.n_tma = (int)(N * eo / 16 * 16 / eo);
+    st = tile(&m0, out, e.out_dtype, (uint64_t)std::max<int64_t>(k.n_tma, 16 / (int64_t)eo), M, (uint64_t)e.ldo * eo);
+    if (!st && epi == EPI_GLU_AUX) {
+      char* g = static_cast<char*>(aux);
+      if (!(st = tile(&m1, g, e.out_dtype, N, M, 2 * N * eo))) st = tile(&m2, g + N * eo, e.out_dtype, N, M, 2 * N * eo);
+    }
+    if (st) return st;
+  }
+  (void)glu;
+
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)p->grid, 1, 1);
+  cfg.blockDim = dim3(kPairThreads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)p->smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t err = cudaLaunchKernelEx(&cfg, reinterpret_cast<PairFn>(const_cast<void*>(p->kernel)), mA, mB, mB2, m0, m1, m2, m3, k);
+  if (err != cudaSuccess) return fail(FL_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(err));
+  if ((st = after_launch(stream, "pair kernel"))) return st;
+  if (!split) return FL_OK;
+
+  GradReduceArgs r{};
+  r.ws = p->d_skws;
+  r.split_stride = split_rows(p) * ws_ld(p);
+  r.ld_ws = ws_ld(p);
+  r.splits = p->split_k;
+  r.residual = residual;
+  r.ldr = e.ldr;
+  r.res_dtype = e.residual_dtype;
+  r.out = out;
+  r.ldo = e.ldo;
+  r.out_dtype = e.out_dtype;
+  r.M = p->M;
+  r.N = (int)p->N;
+  r.nvec = (int)cdiv(p->N, 4);
+  r.scale = e.scale;
+  const int64_t work = p->M * (int64_t)r.nvec;
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(cdiv(work, 256), (int64_t)p->num_sms * 8));
+  err = launch_pdl_b(fl_grad_reduce_kernel, dim3(grid), 256u, stream, r);
+  if (err != cudaSuccess) return fail(FL_ERR_CUDA, "reduction kernel launch: %s", cudaGetErrorString(err));
+  return after_launch(stream, "weight gradient reduction");
+}

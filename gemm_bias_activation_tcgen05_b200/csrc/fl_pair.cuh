@@ -1,0 +1,556 @@
+// fl_pair.cuh — the products of a gated feed-forward block, forward and backward, as one
+// persistent tcgen05 kernel over CTA pairs (256-row UMMA tiles, 16-bit operands, fp32
+// accumulators in tensor memory):
+//
+//   EPI_GLU      h = act(A·Wgᵀ) ⊙ (A·Wuᵀ)                       W = [Wg; Wu] stacked, K contiguous
+//   EPI_GLU_AUX  the same, and g = A·Wgᵀ, u = A·Wuᵀ stored for the backward pass
+//   EPI_DGLU     dh = A·W (W stored [K, N]), then dg = dh·u·act'(g), du = dh·act(g) from the
+//                stored g, u: dh never leaves the chip
+//   EPI_GRAD     y = (Aᵀ·W + residual)·scale, A stored [K, M] and W stored [K, N]: the weight
+//                gradient, K the tokens.  Both operands are read as they lie, through MN-major UMMA
+//                descriptors, so nothing is transposed in memory.  When the tiles leave pairs idle, K
+//                is cut into splits whose fp32 partial tiles go to a workspace, which
+//                fl_grad_reduce_kernel adds in split order.
+//
+// Roles (320 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM allocator and (rank 0 of
+// the pair) UMMA issuer, warps 2..9 epilogue, two per TMEM lane quarter, each with half of the
+// tile's columns in blocks of 32.  Two accumulators, so that a tile's epilogue runs under the next
+// tile's products.  Stages are 64 deep in K: 32 KB a CTA, which leaves up to 64 KB for the epilogue's
+// tiles, which come and go by TMA (32 rows x 32 columns a block).
+//
+// Every wait is bounded; on expiry the kernel records an error code and unwinds.
+#pragma once
+#include "fl_gemm.cuh"
+
+namespace fl {
+
+enum PairEpi : int { EPI_GLU = 0, EPI_GLU_AUX = 1, EPI_DGLU = 2, EPI_GRAD = 3 };
+enum GateAct : int { GATE_SWIGLU = 0, GATE_GEGLU_TANH = 1 };
+
+constexpr int kPairThreads = (kEpiWarp0 + 8) * 32;
+constexpr int kPairBk = 64;                       // K elements of a stage
+constexpr uint32_t kPairABytes = 128u * 128u;     // A: this CTA's 128 rows x 64
+constexpr uint32_t kPairBox = 64u * 128u;         // one MN-major box: 64 columns x 64 K rows
+constexpr int kPairBars = 2 * 12 + 6 + 16;        // at most 12 stages; 16: two per epilogue warp
+constexpr uint32_t kPairBarBytes = 8u * (uint32_t)kPairBars;
+
+// bytes of one 32 x 32 block of a type, and of one epilogue warp's blocks: GLU and GRAD two in turn,
+// GLU_AUX one of each of h, g and u, DGLU two pairs (g and u, overwritten by dg and du)
+__host__ __device__ constexpr uint32_t pair_block_bytes(int out) { return out == DT_F32 ? 4096u : 2048u; }
+__host__ __device__ constexpr uint32_t pair_warp_staging(int epi, int out) {
+  return pair_block_bytes(out) * (epi == EPI_GLU_AUX ? 3u : epi == EPI_DGLU ? 4u : 2u);
+}
+__host__ __device__ constexpr bool pair_a_mn(int epi) { return epi == EPI_GRAD; }
+__host__ __device__ constexpr bool pair_b_mn(int epi) { return epi == EPI_DGLU || epi == EPI_GRAD; }
+
+// σ(y) = 1/(1 + e^(-y)); e^(-y) and the reciprocal on the special-function unit (relative errors
+// near 2^-22), saturating to 0 and 1
+__device__ __forceinline__ float sigmoid_f(float y) { return rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * y)); }
+// The tanh GELU is x·σ(2c(x + 0.044715x³)), c = √(2/π), because (1 + tanh y)/2 = σ(2y): no
+// cancellation for negative x, so that both gates keep fp32 precision over their whole range.
+// act(x), and in `slope` act'(x) = σ + x·σ·(1 − σ)·y'(x)
+template <int ACT>
+__device__ __forceinline__ float gate_f(float x, float& slope) {
+  if constexpr (ACT == GATE_SWIGLU) {
+    const float s = sigmoid_f(x);
+    slope = s * fmaf(x, 1.0f - s, 1.0f);
+    return x * s;
+  } else {
+    constexpr float k = 2.0f * 0.79788456080286536f;
+    const float x2 = x * x;
+    const float s = sigmoid_f(k * x * fmaf(0.044715f, x2, 1.0f));
+    slope = s * fmaf(x * (1.0f - s), k * fmaf(3.0f * 0.044715f, x2, 1.0f), 1.0f);
+    return x * s;
+  }
+}
+
+// Item i of a pair: its tile (and K split): units u = pair, pair + pairs, ... of tiles·splits,
+// split-major, so that pairs that run together share operand panels in L2.
+struct PairItem {
+  int ta, tb, split, kb0, kb1;
+};
+__device__ __forceinline__ bool pair_item(const KParams& p, int cl, int ncl, int i, PairItem& it) {
+  if (i >= p.dp_q + (cl < p.dp_r ? 1 : 0)) return false;
+  int u = cl + i * ncl;
+  it.split = 0;
+  it.kb0 = 0;
+  it.kb1 = p.num_kb;
+  if (p.split_k > 1) {
+    const int tiles = p.tiles_a * p.tiles_b;
+    it.split = u / tiles;
+    u -= it.split * tiles;
+    it.kb0 = (int)((long long)p.num_kb * it.split / p.split_k);
+    it.kb1 = (int)((long long)p.num_kb * (it.split + 1) / p.split_k);
+  }
+  tile_coords(u, p, it.ta, it.tb);
+  return true;
+}
+
+// A block of 32 rows x 32 columns in shared memory as TMA lays it out: lane = row; 16-bit types
+// 64 bytes a row with the 64-byte swizzle, fp32 128 bytes a row with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t blk16_addr(uint32_t base, int lane, int c) {
+  return base + (uint32_t)lane * 64u + (uint32_t)((c ^ ((lane >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ uint32_t blk32_addr(uint32_t base, int lane, int c) {
+  return base + (uint32_t)lane * 128u + (uint32_t)((c ^ (lane & 7)) << 4);
+}
+__device__ __forceinline__ void st_shared_u4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+// this lane's 32 values into a block, in OUT type
+template <int OUT>
+__device__ __forceinline__ void put_block(uint32_t base, int lane, const float (&v)[32]) {
+  if constexpr (OUT == DT_F32) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      st_shared_u4(blk32_addr(base, lane, c), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                   __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      st_shared_u4(blk16_addr(base, lane, c), pack2<OUT>(v[8 * c], v[8 * c + 1]), pack2<OUT>(v[8 * c + 2], v[8 * c + 3]),
+                   pack2<OUT>(v[8 * c + 4], v[8 * c + 5]), pack2<OUT>(v[8 * c + 6], v[8 * c + 7]));
+  }
+}
+template <int DT>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (DT == DT_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// 32 elements of a row of type dt from column n0 by plain (coherent) loads, since the output may be
+// the same buffer; zeros past N
+__device__ __forceinline__ void load_res32(float (&r)[32], const void* base, long long row_off, int n0, int N, int dt) {
+  if (n0 + 32 <= N) {
+    if (dt == DT_F32) {
+      const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + row_off + n0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 f = q[i];
+        r[4 * i] = f.x, r[4 * i + 1] = f.y, r[4 * i + 2] = f.z, r[4 * i + 3] = f.w;
+      }
+    } else {
+      const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + row_off + n0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 v = q[i];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = dt == DT_BF16 ? unpack2<DT_BF16>(w[e]) : unpack2<DT_F16>(w[e]);
+          r[8 * i + 2 * e] = f.x, r[8 * i + 2 * e + 1] = f.y;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      r[j] = 0.0f;
+      if (n0 + j < N) {
+        const long long i = row_off + n0 + j;
+        if (dt == DT_F32) r[j] = reinterpret_cast<const float*>(base)[i];
+        else if (dt == DT_BF16) r[j] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[i]);
+        else r[j] = __half2float(reinterpret_cast<const __half*>(base)[i]);
+      }
+    }
+  }
+}
+
+// Tensor maps: tmA, tmB operands (GLU: tmB gate rows, tmB2 up rows).  tm0..tm3 the epilogue's:
+//   GLU      tm0 h            GLU_AUX  tm0 h, tm1 g, tm2 u
+//   DGLU     tm0 g, tm1 u (loads), tm2 dg, tm3 du        GRAD  tm0 y (or the workspace)
+// p.M is the number of output rows (GRAD with splits: rows of one split, padded to whole tiles), p.N
+// its columns; columns from p.n_tma on (a ragged end below 16 bytes) are stored one by one.
+template <int EPI, int ACT, int OUT>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    fl_pair_tcgen05(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tm0,
+                    const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2,
+                    const __grid_constant__ CUtensorMap tm3, const __grid_constant__ KParams p) {
+  constexpr bool GLU = EPI == EPI_GLU || EPI == EPI_GLU_AUX;
+  constexpr bool A_MN = pair_a_mn(EPI), B_MN = pair_b_mn(EPI);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int NS = p.num_stages;
+  const uint32_t bars = smem_base + p.bar_off;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (NS + s); };
+  auto tfull_bar = [&](int b) { return bars + 8u * (2 * NS + b); };
+  auto tempty_bar = [&](int b) { return bars + 8u * (2 * NS + 2 + b); };
+  const uint32_t drain_bar = bars + 8u * (2 * NS + 4);
+  const uint32_t tmem_slot = bars + 8u * (2 * NS + 5);
+  auto aux_bar = [&](int w, int b) { return bars + 8u * (2 * NS + 6 + 2 * w + b); };  // DGLU: g, u of a block
+
+  const uint32_t rank = cluster_ctarank();
+  const int cluster_id = blockIdx.x >> 1;
+  const int num_clusters = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 16);  // the epilogue warps of both CTAs
+    }
+    mbar_init(drain_bar, 1);
+    if constexpr (EPI == EPI_DGLU)
+      for (int i = 0; i < 16; ++i) mbar_init(aux_bar(i >> 1, i & 1), 1);
+    fence_mbarrier_init();
+    if (p.num_kb > 0) {  // with K = 0 the operand maps are left unencoded and never used
+      prefetch_tensormap(&tmA);
+      prefetch_tensormap(&tmB);
+      if (GLU) prefetch_tensormap(&tmB2);
+    }
+    prefetch_tensormap(&tm0);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, p.tmem_cols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync_all();
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(__cvta_shared_to_generic(tmem_slot));
+
+  if (warp == 0) {
+    // ================================================================ TMA producer
+    if (lane == 0) {
+      uint32_t it = 0;
+      StageRing rs;
+      bool ok = true;
+      PairItem itm;
+      for (int ii = 0; ok && pair_item(p, cluster_id, num_clusters, ii, itm); ++ii) {
+        const int a_row = itm.ta * 256 + (int)rank * 128;
+        const int b_row = GLU ? itm.tb * p.out_tile_n : itm.tb * p.mma_n + (int)rank * (p.mma_n / 2);
+        const CUtensorMap* mb = (GLU && rank != 0) ? &tmB2 : &tmB;
+        for (int kb = itm.kb0; kb < itm.kb1; ++kb, ++it, rs.next((uint32_t)NS)) {
+          const int s = (int)rs.s;
+          if (!wait_bounded(empty_bar(s), rs.ph ^ 1u, p)) { ok = false; break; }
+          const uint32_t sa = smem_base + (uint32_t)s * p.stage_stride;
+          const uint32_t sb = sa + kPairABytes;
+          const uint32_t fb = mapa_shared(full_bar(s), 0);  // both CTAs' bytes complete on the leader's barrier
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2u * p.stage_bytes);
+          const int k0 = kb * kPairBk;
+          if constexpr (A_MN) {
+            tma_load_2d_pair(sa, &tmA, fb, a_row, k0);
+            tma_load_2d_pair(sa + kPairBox, &tmA, fb, a_row + 64, k0);
+          } else {
+            tma_load_2d_pair(sa, &tmA, fb, k0, a_row);
+          }
+          if constexpr (B_MN) {
+            for (int i = 0; i < p.b_boxes; ++i) tma_load_2d_pair(sb + (uint32_t)i * kPairBox, mb, fb, b_row + 64 * i, k0);
+          } else {
+            tma_load_2d_pair(sb, mb, fb, k0, b_row);
+          }
+        }
+      }
+      // Never leave with copies in flight: the leader waits (bounded) for the last fill of every
+      // stage; the final cluster barrier keeps the peer resident until then.
+      for (uint32_t s = 0; rank == 0 && s < (uint32_t)NS && s < it; ++s) {
+        const uint32_t last = it - 1u - ((it - 1u - s) % (uint32_t)NS);
+        (void)wait_bounded(full_bar((int)s), (last / (uint32_t)NS) & 1u, p);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ================================================================ UMMA issuer (rank 0 for both CTAs)
+    if (lane == 0 && rank == 0) {
+      const uint64_t da0 = sdesc_sw128(smem_base, A_MN ? kPairBox : 16u, 1024);
+      const uint64_t db0 = sdesc_sw128(smem_base + kPairABytes, B_MN ? kPairBox : 16u, 1024);
+      const uint64_t stage_step = p.stage_stride >> 4;
+      // a UMMA step is 16 deep: 32 bytes along a K-major row, 16 K rows of 128 bytes in an MN-major box
+      constexpr uint32_t ak = (A_MN ? 2048u : 32u) >> 4, bk = (B_MN ? 2048u : 32u) >> 4;
+      const uint32_t idesc = p.idesc;
+      uint32_t local = 0;
+      StageRing rs;
+      bool ok = true, issued = false;
+      PairItem itm;
+      for (; ok && pair_item(p, cluster_id, num_clusters, (int)local, itm); ++local) {
+        const uint32_t buf = local & 1u;
+        if (!wait_bounded(tempty_bar(buf), ((local >> 1) & 1u) ^ 1u, p, true)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + buf * (uint32_t)p.mma_n;
+        for (int kb = itm.kb0; kb < itm.kb1; ++kb, rs.next((uint32_t)NS)) {
+          const int s = (int)rs.s;
+          if (!wait_bounded(full_bar(s), rs.ph, p)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t da = da0 + (uint64_t)s * stage_step;
+          const uint64_t db = db0 + (uint64_t)s * stage_step;
+#pragma unroll
+          for (int k = 0; k < kPairBk / 16; ++k)
+            umma_f16_pair(d_tmem, da + k * ak, db + k * bk, idesc, (kb > itm.kb0 || k > 0) ? 1u : 0u);
+          umma_commit_pair_both(empty_bar(s));
+          issued = true;
+        }
+        if (!ok) break;
+        if (itm.kb1 > itm.kb0) {
+          umma_commit_pair_both(tfull_bar(buf));
+        } else {
+          mbar_arrive(tfull_bar(buf));
+          mbar_arrive_remote(mapa_shared(tfull_bar(buf), 1));
+        }
+      }
+      if (issued) {  // no MMA may still be running when TMEM is released
+        umma_commit_pair(drain_bar);
+        (void)wait_bounded(drain_bar, 0, p);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ================================================================ epilogue
+    const int q = warp & 3;  // TMEM lane quarter this warp may access
+    const int ew = warp - kEpiWarp0;
+    const int half_cols = p.out_tile_n >> 1;
+    const int c_begin = (ew >> 2) * half_cols;
+    const int nblk = half_cols / 32;
+    const uint32_t stg = smem_base + p.staging_off + (uint32_t)ew * pair_warp_staging(EPI, OUT);
+    uint32_t local = 0;
+    uint32_t blk = 0;  // blocks this warp has begun (DGLU: the g, u tiles alternate between two buffers)
+    bool ok = true;
+    PairItem itm;
+    // DGLU: lane 0 sends for the g and u tiles of block b of an item into buffer `to`
+    auto fetch_gu = [&](const PairItem& w, int b, uint32_t to) {
+      const int n0 = w.tb * p.out_tile_n + c_begin + 32 * b, r0 = w.ta * 256 + (int)rank * 128 + q * 32;
+      mbar_arrive_expect_tx(aux_bar(ew, (int)to), 4096u);
+      tma_load_2d(stg + to * 4096u, &tm0, aux_bar(ew, (int)to), n0, r0);
+      tma_load_2d(stg + to * 4096u + 2048u, &tm1, aux_bar(ew, (int)to), n0, r0);
+    };
+    uint32_t fetched = 0;  // DGLU: blocks whose tiles have been sent for
+    bool more = pair_item(p, cluster_id, num_clusters, 0, itm);
+    if constexpr (EPI == EPI_DGLU) {
+      if (more) {
+        if (lane == 0) fetch_gu(itm, 0, 0);
+        fetched = 1;
+      }
+    }
+    while (more) {
+      PairItem nxt;
+      const bool have_next = pair_item(p, cluster_id, num_clusters, (int)local + 1, nxt);
+      const uint32_t buf = local & 1u;
+      const bool acc_any = itm.kb1 > itm.kb0;
+      const int row0 = itm.ta * 256 + (int)rank * 128 + q * 32;
+      const int m = row0 + lane;
+      const bool m_ok = m < p.M;
+      const int n_tile0 = itm.tb * p.out_tile_n;
+      if (!warp_wait_bounded(tfull_bar(buf), (local >> 1) & 1u, p, lane, true)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + buf * (uint32_t)p.mma_n;
+#pragma unroll 1
+      for (int b = 0; b < nblk; ++b, ++blk) {
+        const int cb = c_begin + 32 * b;
+        const int n0 = n_tile0 + cb;
+        uint32_t ga[32], gu[32];
+        if (acc_any) {
+          tmem_ld32(tacc + (uint32_t)cb, ga);
+          if constexpr (GLU) tmem_ld32(tacc + (uint32_t)(p.out_tile_n + cb), gu);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) ga[j] = gu[j] = 0u;
+        }
+        if constexpr (EPI == EPI_DGLU) {
+          const uint32_t slot = blk & 1u;
+          const uint32_t sg = stg + slot * 4096u, su = sg + 2048u;
+          // the other buffer's stores have read it: send for the next block's tiles
+          const bool last = b + 1 == nblk;
+          if (!last || have_next) {
+            if (lane == 0) {
+              bulk_wait_group_read<0>();
+              if (last) fetch_gu(nxt, 0, slot ^ 1u);
+              else fetch_gu(itm, b + 1, slot ^ 1u);
+            }
+            ++fetched;
+          }
+          if (acc_any) tmem_wait_ld();
+          if (!warp_wait_bounded(aux_bar(ew, (int)slot), (blk >> 1) & 1u, p, lane)) { ok = false; break; }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t ag = blk16_addr(sg, lane, c), au = blk16_addr(su, lane, c);
+            const uint4 g4 = ld_shared_u4(ag), u4 = ld_shared_u4(au);
+            const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+            uint32_t dg[4], du[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 g = unpack2<OUT>(gw[e]), u = unpack2<OUT>(uw[e]);
+              const float h0 = __uint_as_float(ga[8 * c + 2 * e]), h1 = __uint_as_float(ga[8 * c + 2 * e + 1]);
+              float s0, s1;
+              const float a0 = gate_f<ACT>(g.x, s0), a1 = gate_f<ACT>(g.y, s1);
+              dg[e] = pack2<OUT>(h0 * u.x * s0, h1 * u.y * s1);
+              du[e] = pack2<OUT>(h0 * a0, h1 * a1);
+            }
+            st_shared_u4(ag, dg[0], dg[1], dg[2], dg[3]);
+            st_shared_u4(au, du[0], du[1], du[2], du[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (n0 < p.N) {
+              tma_store_2d(&tm2, sg, n0, row0);
+              tma_store_2d(&tm3, su, n0, row0);
+            }
+            bulk_commit_group();
+          }
+        } else {
+          if (acc_any) tmem_wait_ld();
+          float v[32];
+          if constexpr (GLU) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float slope;
+              v[j] = gate_f<ACT>(__uint_as_float(ga[j]), slope) * __uint_as_float(gu[j]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ga[j]);
+            if (p.residual != nullptr && m_ok && n0 < p.N) {
+              float r[32];
+              load_res32(r, p.residual, (long long)m * p.ldr, n0, p.N, p.res_dtype);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += r[j];
+            }
+            if (p.scale != 1.0f) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] *= p.scale;
+            }
+          }
+          // the buffer's last store has read it (GLU_AUX: one buffer of three tiles; else two in turn)
+          const uint32_t sv = EPI == EPI_GLU_AUX ? stg : stg + (blk & 1u) * pair_block_bytes(OUT);
+          if (lane == 0) {
+            if constexpr (EPI == EPI_GLU_AUX) bulk_wait_group_read<0>();
+            else bulk_wait_group_read<1>();
+          }
+          __syncwarp();
+          put_block<OUT>(sv, lane, v);
+          if constexpr (EPI == EPI_GLU_AUX) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ga[j]);
+            put_block<OUT>(sv + 2048u, lane, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(gu[j]);
+            put_block<OUT>(sv + 4096u, lane, v);
+          } else if (n0 + 32 > p.n_tma && n0 < p.N && m_ok) {
+            // ragged row end: a TMA store writes whole 16-byte granules
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (n0 + j >= p.n_tma && n0 + j < p.N) store_elem<OUT>(p.out, (long long)m * p.ldo + n0 + j, v[j]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (n0 < p.n_tma) {
+              tma_store_2d(&tm0, sv, n0, itm.split * p.split_rows + row0);
+              if constexpr (EPI == EPI_GLU_AUX) {
+                tma_store_2d(&tm1, sv + 2048u, n0, row0);
+                tma_store_2d(&tm2, sv + 4096u, n0, row0);
+              }
+            }
+            bulk_commit_group();
+          }
+        }
+        if (b + 1 == nblk) {
+          // this warp's TMEM reads of the tile are done: hand its share back to the leader
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (rank != 0) mbar_arrive_remote(mapa_shared(tempty_bar(buf), 0));
+            else mbar_arrive(tempty_bar(buf));
+          }
+        }
+      }
+      if (!ok) break;
+      ++local;
+      itm = nxt;
+      more = have_next;
+    }
+    if constexpr (EPI == EPI_DGLU) {
+      // after a wait that gave up: no tile may still be on its way when the CTA leaves
+      for (uint32_t f = blk; f < fetched; ++f) (void)warp_wait_bounded(aux_bar(ew, (int)(f & 1u)), (f >> 1) & 1u, p, lane);
+    }
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  }
+
+  // ================================================================ teardown
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, p.tmem_cols);
+  }
+}
+
+// y[m,n] = (Σ_s ws[s][m][n] + residual[m,n])·scale over the S fp32 partial tiles, in split order.
+// A thread takes four columns of a row; rows of the workspace are 16-byte aligned.
+struct GradReduceArgs {
+  const float* ws;
+  long long split_stride, ld_ws;
+  int splits;
+  const void* residual;
+  long long ldr;
+  int res_dtype;
+  void* out;
+  long long ldo;
+  int out_dtype;
+  long long M;
+  int N, nvec;
+  float scale;
+};
+__global__ void __launch_bounds__(256) fl_grad_reduce_kernel(const GradReduceArgs P) {
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
+  const long long total = P.M * P.nvec;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
+    const long long m = i / P.nvec;
+    const int n0 = 4 * (int)(i - m * P.nvec);
+    const float4* w = reinterpret_cast<const float4*>(P.ws + m * P.ld_ws + n0);
+    float4 a = __ldcg(w);
+    for (int s0 = 1; s0 < P.splits; s0 += 4) {
+      float4 t[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        t[k] = s0 + k < P.splits ? __ldcg(w + (long long)(s0 + k) * (P.split_stride / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a.x += t[k].x, a.y += t[k].y, a.z += t[k].z, a.w += t[k].w;
+    }
+    float v[4] = {a.x, a.y, a.z, a.w};
+    const int cnt = min(4, P.N - n0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= cnt) break;
+      if (P.residual != nullptr) {
+        const long long o = m * P.ldr + n0 + j;
+        v[j] += P.res_dtype == DT_F32    ? reinterpret_cast<const float*>(P.residual)[o]
+                : P.res_dtype == DT_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(P.residual)[o])
+                                         : __half2float(reinterpret_cast<const __half*>(P.residual)[o]);
+      }
+      v[j] *= P.scale;
+    }
+    // (rows of y start on 16 bytes, so four whole columns are one store)
+    const long long o = m * P.ldo + n0;
+    if (cnt == 4 && P.out_dtype == DT_F32) {
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(P.out) + o) = make_float4(v[0], v[1], v[2], v[3]);
+    } else if (cnt == 4) {
+      const uint2 h = P.out_dtype == DT_BF16 ? make_uint2(pack2<DT_BF16>(v[0], v[1]), pack2<DT_BF16>(v[2], v[3]))
+                                             : make_uint2(pack2<DT_F16>(v[0], v[1]), pack2<DT_F16>(v[2], v[3]));
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(P.out) + o) = h;
+    } else {
+      for (int j = 0; j < cnt; ++j) {
+        if (P.out_dtype == DT_F32) store_elem<DT_F32>(P.out, o + j, v[j]);
+        else if (P.out_dtype == DT_BF16) store_elem<DT_BF16>(P.out, o + j, v[j]);
+        else store_elem<DT_F16>(P.out, o + j, v[j]);
+      }
+    }
+  }
+}
+
+}  // namespace fl

@@ -74,7 +74,29 @@ typedef enum { FL_COMPUTE_32F = 0, FL_COMPUTE_32F_3XTF32 = 1 } fl_compute;
  *   GELU_AUX_BIAS   as GELU_BIAS, and aux = v = acc + bias stored in the output type, the
  *                   input of the GELU backward (fl_dgelu_bgrad); [epilog] keeps forward
  *                   state for the backward pass, [gelu] §2.2.1 fuses the backward too
- * Every kind may add a residual and scale: y = (act(v) + residual)·scale. */
+ * Every kind up to here may add a residual and scale: y = (act(v) + residual)·scale.
+ *
+ * The gated feed-forward block in training ([mlp] gives its forward; no backward on the pages).
+ * act is x·σ(x) (SWIGLU) or the tanh GELU (GEGLU); 16-bit operands and results:
+ *   SWIGLU          W is the stacked [2N, K] matrix [Wg; Wu]; y = act(A·Wgᵀ)·(A·Wuᵀ)
+ *   GEGLU_TANH_AUX, SWIGLU_AUX
+ *                   the same, and aux = [A·Wgᵀ, A·Wuᵀ] stored as [M, 2N] (packed) in the output
+ *                   type; N a multiple of 8
+ *   DGEGLU_TANH, DSWIGLU
+ *                   the backward through the gate, fused into the product that brings the
+ *                   gradient: A = dy [M, K], W = the down projection's weight stored [K, N]
+ *                   (b_major 1), aux = the forward's [M, 2N], read only; with dh = A·W, which is
+ *                   never stored or rounded, out [M, ldo], ldo ≥ 2N (0: 2N), is
+ *                   [dh·u·act'(g), dh·act(g)]; N a multiple of 8.  out may be aux's own buffer
+ *                   when ldo is 2N.  (The gradient of the block's input is then the NONE layer
+ *                   out·[Wg; Wu] with b_major 1 and 2N as its K.)
+ *   WGRAD           a weight gradient, y = (Aᵀ·W + residual)·scale: A stored [K, M] (lda ≥ M), W
+ *                   stored [K, N] (b_major 1), K the number of tokens, any out_dtype.  The
+ *                   residual (has_residual) is an earlier gradient to add to; it may be out's own
+ *                   buffer, with the same type and pitch.  Sums are in fp32, in an order that
+ *                   depends on the shape and the GPU alone.
+ * These take no bias, no unfused twin, FL_SCHED_AUTO only, and, but for WGRAD, no residual and no
+ * scale. */
 typedef enum {
   FL_EPI_NONE = 0,
   FL_EPI_BIAS = 1,
@@ -84,7 +106,13 @@ typedef enum {
   FL_EPI_GELU_TANH_BIAS = 5,
   FL_EPI_GEGLU_TANH = 6,
   FL_EPI_GELU_AUX_BIAS = 7,
-  FL_EPI_GELU_SIGMOID_BIAS = 8
+  FL_EPI_GELU_SIGMOID_BIAS = 8,
+  FL_EPI_SWIGLU = 9,
+  FL_EPI_GEGLU_TANH_AUX = 10,
+  FL_EPI_SWIGLU_AUX = 11,
+  FL_EPI_DGEGLU_TANH = 12,
+  FL_EPI_DSWIGLU = 13,
+  FL_EPI_WGRAD = 14
 } fl_epi_kind;
 
 /* The "epilog" argument of fl_plan.  Zero-initialise, then set fields. */
@@ -128,12 +156,13 @@ typedef struct fl_plan_s* fl_plan_t;
  * of an unfused plan; and, when the shape's tiles leave the last round of CTA pairs
  * partly idle (16-bit operands, M > 128), the stream-K workspace: one fp32 partial
  * accumulator of 32 rows x mma_n/2 columns per CTA and epilogue warp (at most
- * 148 x 8 x 16 KB = 19.4 MB on a B200) and its flags.  Every execute of the plan
+ * 148 x 8 x 16 KB = 19.4 MB on a B200) and its flags; for WGRAD, when its tiles would leave CTA
+ * pairs idle, the fp32 partial results of up to 32 K splits.  Every execute of the plan
  * reuses this workspace, so two executes of one plan must not overlap on the GPU.
  * Needs the target device current.
  *   out     receives the plan handle (host pointer, must not be NULL)
  *   M, N, K ≥ 1 for M and N, ≥ 0 for K (K = 0 gives y = epi(0 + bias)); for
- *           GEGLU_TANH, N is the width of h and W has 2N rows
+ *           GEGLU_TANH, SWIGLU and their AUX kinds, N is the width of h and W has 2N rows
  *   dtype   fl_dtype of A and W (F16/BF16 with FL_COMPUTE_32F, F32 with 3XTF32)
  * Errors: FL_ERR_INVALID_ARG, FL_ERR_UNSUPPORTED, FL_ERR_DEVICE, FL_ERR_OOM. */
 fl_status fl_plan(fl_plan_t* out, int64_t M, int64_t N, int64_t K, int32_t dtype,
@@ -142,12 +171,14 @@ fl_status fl_plan(fl_plan_t* out, int64_t M, int64_t N, int64_t K, int32_t dtype
 /* Run the planned layer on `stream` (a cudaStream_t; NULL = legacy default stream)
  * ([epilog] execute(): one kernel launch for a fused plan).
  *   A        [M, lda] operand
- *   W        [N, ldb] weight (b_major 0), [K, ldb] (b_major 1) or [2N, ldb] (GEGLU)
+ *   W        [N, ldb] weight (b_major 0), [K, ldb] (b_major 1) or [2N, ldb] (GEGLU, SWIGLU)
  *   bias     length N (bias_axis 0) or M (bias_axis 1); required iff the kind has a bias
  *   aux      RELU_AUX_BIAS: [M, ceil(N/32)] uint32, packed rows; bit j of word w of
  *            row m is column 32w+j, least significant bit first; bits of columns ≥ N
  *            are written as 0.  GELU_AUX_BIAS: [M, ldo] in the output type (16-byte
- *            aligned), the pre-activation v.  Null for every other kind
+ *            aligned), the pre-activation v.  GEGLU_TANH_AUX, SWIGLU_AUX (written) and
+ *            DGEGLU_TANH, DSWIGLU (read): [M, 2N] packed, 16-byte aligned.  Null for every
+ *            other kind
  *   residual [M, ldr], required iff has_residual
  *   out      [M, ldo] result
  * Errors: FL_ERR_INVALID_ARG (missing operand), FL_ERR_ALIGNMENT, FL_ERR_CUDA. */
@@ -291,7 +322,7 @@ typedef struct {
   int32_t tile_m, tile_n;      /* output tile of one CTA (before split-K) */
   int32_t mma_n;               /* tensor-core N per instruction */
   int32_t swap_ab;             /* 1: W is the tensor-core A operand (small M) */
-  int32_t split_k;             /* CTAs of a cluster sharing one tile along K */
+  int32_t split_k;             /* CTAs of a cluster sharing one tile along K; WGRAD: splits of K */
   int32_t stages;              /* shared-memory pipeline depth */
   int32_t grid;                /* CTAs launched by the main kernel */
   int32_t smem_bytes;          /* dynamic shared memory per CTA */
@@ -340,6 +371,7 @@ const char* fl_last_error(void);
  *   - The error word is cleared at each call and not read back: a bounded
  *     in-kernel wait that gives up is not reported by this entry point.
  *   - fp16/bf16 operands with FL_COMPUTE_32F only.
+ *   - WGRAD runs without K splits, which need a workspace: slower when it has few tiles.
  * Errors: as fl_plan and fl_execute. */
 fl_status fl_execute_noalloc(int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t compute,
                              const fl_epilogue_desc* epi, const void* A, const void* W,

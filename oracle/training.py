@@ -74,22 +74,28 @@ def dropout_layernorm_backward(dz, dsum, s, mean, rstd, gamma, p=0.0, seed=0, of
     return ds, dropout(ds, p, seed, offset), (dz * u).sum(axis=0), dz.sum(axis=0)
 
 
+def _logistic(kind: str, v: np.ndarray):
+    """(σ(y), σ(-y), y') of the gate v·σ(y).  SWIGLU: y = v.  GEGLU_TANH: (1 + tanh w)/2 = σ(2w), so y = 2w with
+    w = √(2/π)·(v + 0.044715·v³); in this form nothing cancels where tanh w is near -1."""
+    if kind == "SWIGLU":
+        y, dy = v, np.ones_like(v)
+    else:
+        c = 2.0 * math.sqrt(2.0 / math.pi)
+        y, dy = c * (v + 0.044715 * v**3), c * (1.0 + 3.0 * 0.044715 * v * v)
+    with np.errstate(over="ignore"):
+        return 1.0 / (1.0 + np.exp(-y)), 1.0 / (1.0 + np.exp(y)), dy
+
+
 def gate(v, kind: str) -> np.ndarray:
     """The gate's activation: v·σ(v) (SWIGLU) or the tanh GELU (GEGLU_TANH)."""
     v = np.asarray(v, np.float64)
-    if kind == "SWIGLU":
-        return v / (1.0 + np.exp(-v))
-    return 0.5 * v * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (v + 0.044715 * v**3)))
+    return v * _logistic(kind, v)[0]
 
 
 def gate_grad(v, kind: str) -> np.ndarray:
     v = np.asarray(v, np.float64)
-    if kind == "SWIGLU":
-        s = 1.0 / (1.0 + np.exp(-v))
-        return s * (1.0 + v * (1.0 - s))
-    c = math.sqrt(2.0 / math.pi)
-    t = np.tanh(c * (v + 0.044715 * v**3))
-    return 0.5 * (1.0 + t) + 0.5 * v * (1.0 - t * t) * c * (1.0 + 3.0 * 0.044715 * v * v)
+    s, t, dy = _logistic(kind, v)
+    return s + v * s * t * dy
 
 
 def glu(x, W, kind: str):

@@ -98,3 +98,55 @@ def test_workspace_refusals(fl):
     assert fl.LIB.fl_layernorm_grad_workspace_size(4, 4, None) == fl.FL_ERR_INVALID_ARG
     assert fl.LIB.fl_layernorm_grad_workspace_size(-1, 4, ctypes.byref(n)) == fl.FL_ERR_INVALID_ARG
     assert fl.LIB.fl_layernorm_grad_workspace_size(4, 2**31, ctypes.byref(n)) == fl.FL_ERR_INVALID_ARG
+
+
+# ---------------------------------------------------------------- the gated linear units and the weight gradient
+def _plan(fl, kind, M=256, N=256, K=64, dtype="bf16", **epi):
+    e = fl.make_epilogue(kind=kind, **epi)
+    info = fl.fl_plan_info()
+    st = fl.LIB.fl_plan_preview(M, N, K, fl.DTYPES[dtype], fl.COMPUTES["32F_3XTF32" if dtype == "f32" else "32F"], ctypes.byref(e), 148,
+                                232448, ctypes.byref(info))
+    return st, info
+
+
+@pytest.mark.parametrize("kind,kw,status", [
+    ("SWIGLU", dict(b_major=1), "FL_ERR_UNSUPPORTED"), ("SWIGLU", dict(out_dtype="f32"), "FL_ERR_UNSUPPORTED"),
+    ("SWIGLU", dict(dtype="f32"), "FL_ERR_UNSUPPORTED"), ("SWIGLU", dict(unfused=True), "FL_ERR_UNSUPPORTED"),
+    ("SWIGLU", dict(has_residual=True), "FL_ERR_UNSUPPORTED"), ("SWIGLU", dict(scale=0.5), "FL_ERR_UNSUPPORTED"),
+    ("SWIGLU", dict(schedule="stream_k"), "FL_ERR_UNSUPPORTED"), ("SWIGLU", dict(K=60), "FL_ERR_ALIGNMENT"),
+    ("SWIGLU", dict(N=100, ldo=100), "FL_ERR_ALIGNMENT"), ("SWIGLU", dict(N=100, ldo=104), "FL_OK"),
+    ("SWIGLU_AUX", dict(N=100, ldo=104), "FL_ERR_ALIGNMENT"), ("GEGLU_TANH_AUX", dict(N=104), "FL_OK"),
+    ("DSWIGLU", dict(), "FL_ERR_UNSUPPORTED"), ("DSWIGLU", dict(b_major=1), "FL_OK"),
+    ("DSWIGLU", dict(b_major=1, ldo=504), "FL_ERR_INVALID_ARG"), ("DSWIGLU", dict(b_major=1, N=100, ldb=104, ldo=208), "FL_ERR_ALIGNMENT"),
+    ("DGEGLU_TANH", dict(b_major=1, out_dtype="f32"), "FL_ERR_UNSUPPORTED"), ("DGEGLU_TANH", dict(b_major=1, scale=2.0), "FL_ERR_UNSUPPORTED"),
+    ("WGRAD", dict(), "FL_ERR_UNSUPPORTED"), ("WGRAD", dict(b_major=1, out_dtype="f32", K=77), "FL_OK"),
+    ("WGRAD", dict(b_major=1, lda=248), "FL_ERR_INVALID_ARG"), ("WGRAD", dict(b_major=1, M=250), "FL_ERR_ALIGNMENT"),
+    ("WGRAD", dict(b_major=1, M=250, lda=256, has_residual=True, scale=0.5), "FL_OK"),
+    ("WGRAD", dict(b_major=1, dtype="f32"), "FL_ERR_UNSUPPORTED"), ("WGRAD", dict(b_major=1, K=-1), "FL_ERR_INVALID_ARG"),
+])
+def test_pair_kind_refusals(fl, kind, kw, status):
+    st, _ = _plan(fl, kind, **kw)
+    assert fl.STATUS_NAMES[st] == status, fl.fl_last_error()
+    # fl_execute_noalloc refuses the same, before any device call
+    if st != fl.FL_OK:
+        shape = {k: kw.get(k, d) for k, d in (("M", 256), ("N", 256), ("K", 64))}
+        dtype = kw.get("dtype", "bf16")
+        e = fl.make_epilogue(kind=kind, **{k: v for k, v in kw.items() if k not in ("M", "N", "K", "dtype")})
+        assert fl.LIB.fl_execute_noalloc(shape["M"], shape["N"], shape["K"], fl.DTYPES[dtype],
+                                         fl.COMPUTES["32F_3XTF32" if dtype == "f32" else "32F"], ctypes.byref(e), 16, 16, None, None,
+                                         None, 16, None) == st
+
+
+@pytest.mark.parametrize("kind", ["SWIGLU", "SWIGLU_AUX", "DSWIGLU", "WGRAD"])
+def test_pair_configurations(fl, kind):
+    """Every choice fits the GPU: shared memory, stages, whole pairs, splits no more than K blocks."""
+    import random
+    rng = random.Random(kind)
+    for _ in range(300):
+        M, N, K = (8 * rng.randint(1, 1500) for _ in range(3))
+        st, i = _plan(fl, kind, M, N, K, b_major=int(kind in ("DSWIGLU", "WGRAD")), out_dtype=rng.choice(["bf16", "f16"]))
+        assert st == fl.FL_OK, fl.fl_last_error()
+        if i.cta_pair:
+            assert i.smem_bytes <= 232448 and i.stages >= 3 and i.grid % 2 == 0 and 0 < i.grid <= 148
+            assert 1 <= i.split_k <= max(1, -(-K // 64)) and (kind == "WGRAD" or i.split_k == 1)
+        assert i.launches_per_execute == (2 if kind == "WGRAD" and i.split_k > 1 else 1)
