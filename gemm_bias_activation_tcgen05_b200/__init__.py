@@ -142,10 +142,27 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+def _current_device() -> int:
+    import torch
+    return torch._C._cuda_getDevice()
+
+
+_raw_stream = None  # the current stream's handle by device index, where torch has it
+
+
 def _stream(s) -> Optional[int]:
+    """Handle of a stream; None: torch's current stream (NULL without a GPU).  Read as a plain handle, because
+    making a Stream object took 4.2 of the 9.8 us of a small call."""
+    global _raw_stream
     if s is None:
+        if _raw_stream is not None:
+            return _raw_stream(_current_device())
         import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        if not torch.cuda.is_available():
+            return None
+        handle = torch.cuda.current_stream().cuda_stream  # (initialises CUDA)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return handle
     if isinstance(s, int):
         return s
     return s.cuda_stream

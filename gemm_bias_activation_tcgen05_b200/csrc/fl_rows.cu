@@ -23,8 +23,10 @@ fl_status drop_params(const char* who, const fl_dropout_desc* d, DropParams* out
   if (d->reserved != 0) return fail(FL_ERR_INVALID_ARG, "%s: reserved fields must be 0", who);
   if (reinterpret_cast<uintptr_t>(d->offset_dev) % 8)
     return fail(FL_ERR_ALIGNMENT, "%s: offset_dev must be 8-byte aligned", who);
-  out->k0 = (uint32_t)d->seed;
-  out->k1 = (uint32_t)(d->seed >> 32);
+  for (uint32_t r = 0; r < 10; ++r) {
+    out->k0[r] = (uint32_t)d->seed + r * 0x9E3779B9u;
+    out->k1[r] = (uint32_t)(d->seed >> 32) + r * 0xBB67AE85u;
+  }
   out->offset = d->offset;
   out->offset_dev = d->offset_dev;
   out->threshold = (uint32_t)((double)d->p * 4294967296.0);  // ⌊p·2^32⌋ (p < 1: below 2^32)
@@ -75,30 +77,55 @@ struct RowKernel {
   void (*fn)(Args);
   int threads, vecs, block;  // threads 0: the kernel for rows of any length
 };
+// The types that have kernels of their own: activations in one 16-bit type, with the residual
+// stream in the same type or in fp32.  Everything else runs on the untyped kernels.
+enum RowTypes { ROWS_ANY, ROWS_BF16, ROWS_F16, ROWS_BF16_F32, ROWS_F16_F32 };
+RowTypes row_types(bool whole_vectors, int x, int s, int z) {
+  if (!whole_vectors || x != z || x == FL_F32) return ROWS_ANY;
+  if (s == x) return x == FL_BF16 ? ROWS_BF16 : ROWS_F16;
+  if (s == FL_F32) return x == FL_BF16 ? ROWS_BF16_F32 : ROWS_F16_F32;
+  return ROWS_ANY;
+}
 template <int T, int V>
-RowKernel<DropLnArgs> ln_of() { return {fl_dropout_ln_kernel<T, V>, T, V, T < 128 ? 128 : T}; }
+RowKernel<DropLnArgs> ln_of(RowTypes r) {
+  switch (r) {
+    case ROWS_BF16: return {fl_dropout_ln_kernel<T, V, DT_BF16, DT_BF16, DT_BF16>, T, V, ln_block(T)};
+    case ROWS_F16: return {fl_dropout_ln_kernel<T, V, DT_F16, DT_F16, DT_F16>, T, V, ln_block(T)};
+    case ROWS_BF16_F32: return {fl_dropout_ln_kernel<T, V, DT_BF16, DT_F32, DT_BF16>, T, V, ln_block(T)};
+    case ROWS_F16_F32: return {fl_dropout_ln_kernel<T, V, DT_F16, DT_F32, DT_F16>, T, V, ln_block(T)};
+    default: return {fl_dropout_ln_kernel<T, V, ANY, ANY, ANY>, T, V, ln_block(T)};
+  }
+}
 template <int T, int V>
-RowKernel<DropLnBwdArgs> ln_bwd_of() { return {fl_dropout_ln_bwd_kernel<T, V>, T, V, T < 512 ? 512 : T}; }
+RowKernel<DropLnBwdArgs> ln_bwd_of(RowTypes r) {
+  switch (r) {
+    case ROWS_BF16: return {fl_dropout_ln_bwd_kernel<T, V, DT_BF16, DT_BF16, DT_BF16>, T, V, ln_bwd_block(T)};
+    case ROWS_F16: return {fl_dropout_ln_bwd_kernel<T, V, DT_F16, DT_F16, DT_F16>, T, V, ln_bwd_block(T)};
+    case ROWS_BF16_F32: return {fl_dropout_ln_bwd_kernel<T, V, DT_BF16, DT_F32, DT_BF16>, T, V, ln_bwd_block(T)};
+    case ROWS_F16_F32: return {fl_dropout_ln_bwd_kernel<T, V, DT_F16, DT_F32, DT_F16>, T, V, ln_bwd_block(T)};
+    default: return {fl_dropout_ln_bwd_kernel<T, V, ANY, ANY, ANY>, T, V, ln_bwd_block(T)};
+  }
+}
 
 // Forward: two vectors a thread.
-RowKernel<DropLnArgs> ln_kernel(int64_t N) {
-  if (N <= 512) return ln_of<32, 2>();
-  if (N <= 1024) return ln_of<64, 2>();
-  if (N <= 2048) return ln_of<128, 2>();
-  if (N <= 4096) return ln_of<256, 2>();
-  if (N <= 8192) return ln_of<512, 2>();
-  if (N <= 16384) return ln_of<1024, 2>();
+RowKernel<DropLnArgs> ln_kernel(int64_t N, RowTypes r) {
+  if (N <= 512) return ln_of<32, 2>(r);
+  if (N <= 1024) return ln_of<64, 2>(r);
+  if (N <= 2048) return ln_of<128, 2>(r);
+  if (N <= 4096) return ln_of<256, 2>(r);
+  if (N <= 8192) return ln_of<512, 2>(r);
+  if (N <= 16384) return ln_of<1024, 2>(r);
   return {fl_dropout_ln_long_kernel, 0, 0, 1024};
 }
 // Backward: one vector a thread as far as a CTA goes, since the column sums stay in registers.
-RowKernel<DropLnBwdArgs> ln_bwd_kernel(int64_t N) {
-  if (N <= 256) return ln_bwd_of<32, 1>();
-  if (N <= 512) return ln_bwd_of<64, 1>();
-  if (N <= 1024) return ln_bwd_of<128, 1>();
-  if (N <= 2048) return ln_bwd_of<256, 1>();
-  if (N <= 4096) return ln_bwd_of<512, 1>();
-  if (N <= 8192) return ln_bwd_of<1024, 1>();
-  if (N <= 16384) return ln_bwd_of<1024, 2>();
+RowKernel<DropLnBwdArgs> ln_bwd_kernel(int64_t N, RowTypes r) {
+  if (N <= 256) return ln_bwd_of<32, 1>(r);
+  if (N <= 512) return ln_bwd_of<64, 1>(r);
+  if (N <= 1024) return ln_bwd_of<128, 1>(r);
+  if (N <= 2048) return ln_bwd_of<256, 1>(r);
+  if (N <= 4096) return ln_bwd_of<512, 1>(r);
+  if (N <= 8192) return ln_bwd_of<1024, 1>(r);
+  if (N <= 16384) return ln_bwd_of<1024, 2>(r);
   return {fl_dropout_ln_bwd_long_kernel, 0, 0, 1024};
 }
 
@@ -110,9 +137,9 @@ struct BwdGeom {
   int grid, ws_ld;
   size_t bytes;
 };
-BwdGeom bwd_geom(int64_t M, int64_t N, int sms) {
+BwdGeom bwd_geom(int64_t M, int64_t N, int sms, RowTypes r) {
   BwdGeom g;
-  g.k = ln_bwd_kernel(N);
+  g.k = ln_bwd_kernel(N, r);
   const int64_t ctas = cdiv(M, g.k.threads == 0 ? 1 : g.k.block / g.k.threads);
   g.grid = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)sms * (g.k.block == 1024 ? 1 : 2)));
   g.ws_ld = (int)(cdiv(N, 8) * 8);
@@ -158,10 +185,16 @@ extern "C" fl_status fl_dropout(const void* x, const void* residual, void* y, in
   P.nvec = (int)cdiv(N, 8);
   int sms = 148;
   if ((st = num_sms(&sms))) return st;
-  // two vectors a thread and trip; at most one resident wave of eight 256-thread CTAs per SM
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(cdiv(M * (int64_t)P.nvec, 512), (int64_t)sms * 8));
+  // two vectors a thread and trip; at most one resident wave of four 256-thread CTAs per SM
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(cdiv(M * (int64_t)P.nvec, 512), (int64_t)sms * 4));
+  const RowTypes types = row_types(P.vec && N % 8 == 0, x_dtype, y_dtype, x_dtype);
+  void (*fn)(DropoutArgs) = types == ROWS_BF16       ? fl_dropout_kernel<DT_BF16, DT_BF16>
+                            : types == ROWS_F16      ? fl_dropout_kernel<DT_F16, DT_F16>
+                            : types == ROWS_BF16_F32 ? fl_dropout_kernel<DT_BF16, DT_F32>
+                            : types == ROWS_F16_F32  ? fl_dropout_kernel<DT_F16, DT_F32>
+                                                     : fl_dropout_kernel<ANY, ANY>;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
-  const cudaError_t err = launch_pdl_b(fl_dropout_kernel, dim3((unsigned)grid), 256u, s, P);
+  const cudaError_t err = launch_pdl_b(fn, dim3((unsigned)grid), 256u, s, P);
   if (err != cudaSuccess) return fail(FL_ERR_CUDA, "%s: kernel launch: %s", who, cudaGetErrorString(err));
   return after_launch(s, who);
 }
@@ -202,7 +235,7 @@ extern "C" fl_status fl_dropout_layernorm(const void* x, const void* residual, c
   P.N = (int)N;
   P.param_dt = param_dtype;
   P.eps = eps;
-  const RowKernel<DropLnArgs> k = ln_kernel(N);
+  const RowKernel<DropLnArgs> k = ln_kernel(N, row_types(P.vec && N % 8 == 0, x_dtype, sum_dtype, z_dtype));
   const int64_t ctas = cdiv(M, k.threads == 0 ? 1 : k.block / k.threads);
   size_t smem = 0;
   if ((st = ring_of(k, operand_bytes(P.x, k.vecs, k.block) + operand_bytes(P.r, k.vecs, k.block), &P, &smem))) return st;
@@ -226,7 +259,7 @@ extern "C" fl_status fl_layernorm_grad_workspace_size(int64_t M, int64_t N, size
   if (st) return st;
   int sms = 148;
   if ((st = num_sms(&sms))) return st;
-  *bytes = bwd_geom(M, N, sms).bytes;
+  *bytes = bwd_geom(M, N, sms, ROWS_ANY).bytes;
   return FL_OK;
 }
 
@@ -257,7 +290,8 @@ extern "C" fl_status fl_dropout_layernorm_backward(
     if (reinterpret_cast<uintptr_t>(p) % 4) return fail(FL_ERR_ALIGNMENT, "%s: an fp32 vector is not 4-byte aligned", who);
   int sms = 148;
   if ((st = num_sms(&sms))) return st;
-  const BwdGeom g = bwd_geom(M, N, sms);
+  // (the geometry, and so the workspace, does not depend on the types)
+  const BwdGeom g = bwd_geom(M, N, sms, row_types(P.vec && N % 8 == 0, x_dtype, sum_dtype, z_dtype));
   const bool params = dgamma || dbeta;
   if (params && (!workspace || workspace_bytes < g.bytes || !aligned16(workspace)))
     return fail(FL_ERR_INVALID_ARG, "%s: dgamma and dbeta need a 16-byte aligned workspace of %zu bytes "

@@ -20,8 +20,13 @@ namespace fl {
 // counter is (block, offset), the key the seed; block = m·⌈N/4⌉ + n/4 and word n mod 4 belong to
 // element (m, n), so that the numbers depend on the logical shape only, never on pitches,
 // alignment or the launch.
+//
+// A round is two 32 x 32 -> 64 multiplications and two three-way exclusive ors: the round keys come
+// from the host, so that they are constant-bank operands, and what the first round makes of the
+// offset is the same for every element.  Ten rounds for four elements still are the largest part of
+// these kernels' instructions.
 struct DropParams {
-  uint32_t k0, k1;             // key: the seed's halves
+  uint32_t k0[10], k1[10];     // the rounds' keys, from the seed's halves
   uint64_t offset;             // upper counter half
   const uint64_t* offset_dev;  // added to offset when not null (read on the device)
   uint32_t threshold;          // dropped where the word is below ⌊p·2^32⌋
@@ -29,35 +34,53 @@ struct DropParams {
   int on;                      // 0: p = 0, nothing is drawn
 };
 
-__device__ __forceinline__ uint4 philox4x32_10(uint64_t block, uint64_t offset, uint32_t k0, uint32_t k1) {
-  uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+// What a thread keeps of the offset: the first round's share of the new words 0, 1 and 2.
+struct DropOffset {
+  uint32_t w0, w1, w2;
+};
+__device__ __forceinline__ DropOffset drop_offset(const DropParams& d) {
+  uint64_t off = d.offset;
+  if (d.on && d.offset_dev != nullptr) off += *d.offset_dev;
+  const uint64_t b = (uint64_t)(uint32_t)off * 0xCD9E8D57u;
+  return {(uint32_t)(b >> 32) ^ d.k0[0], (uint32_t)b, (uint32_t)(off >> 32) ^ d.k1[0]};
+}
+
+__device__ __forceinline__ uint4 philox4x32_10(uint64_t block, const DropOffset& o, const DropParams& d) {
+  const uint64_t first = (uint64_t)(uint32_t)block * 0xD2511F53u;
+  uint32_t c0 = o.w0 ^ (uint32_t)(block >> 32), c1 = o.w1, c2 = (uint32_t)(first >> 32) ^ o.w2, c3 = (uint32_t)first;
 #pragma unroll
-  for (int r = 0; r < 10; ++r) {
+  for (int r = 1; r < 10; ++r) {
     const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ d.k0[r];
     c1 = (uint32_t)b;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ d.k1[r];
     c3 = (uint32_t)a;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return make_uint4(c0, c1, c2, c3);
 }
 
-// v[i] = D(v)[i] for the eight elements of blocks `block` and `block` + 1
-__device__ __forceinline__ void drop8(float (&v)[8], uint64_t block, uint64_t offset, const DropParams& d) {
+// r[i] + D(v)[i] for the eight elements of blocks `block` and `block` + 1.  A dropped element adds
+// nothing at all (not 0·v, which would keep a NaN); a kept one is one fused product and sum.
+__device__ __forceinline__ void add_dropped8(float (&r)[8], const float (&v)[8], uint64_t block, const DropOffset& o,
+                                             const DropParams& d) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint4 r = philox4x32_10(block + h, offset, d.k0, d.k1);
-    v[4 * h + 0] = r.x >= d.threshold ? v[4 * h + 0] * d.scale : 0.0f;
-    v[4 * h + 1] = r.y >= d.threshold ? v[4 * h + 1] * d.scale : 0.0f;
-    v[4 * h + 2] = r.z >= d.threshold ? v[4 * h + 2] * d.scale : 0.0f;
-    v[4 * h + 3] = r.w >= d.threshold ? v[4 * h + 3] * d.scale : 0.0f;
+    const uint4 w = philox4x32_10(block + h, o, d);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (x[i] >= d.threshold) r[4 * h + i] = fmaf(v[4 * h + i], d.scale, r[4 * h + i]);
   }
 }
-
-__device__ __forceinline__ uint64_t drop_offset(const DropParams& d) {
-  return d.on && d.offset_dev != nullptr ? d.offset + *d.offset_dev : d.offset;
+// v = D(v)
+__device__ __forceinline__ void drop8(float (&v)[8], uint64_t block, const DropOffset& o, const DropParams& d) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 w = philox4x32_10(block + h, o, d);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * h + i] = x[i] >= d.threshold ? v[4 * h + i] * d.scale : 0.0f;
+  }
 }
 
 // ---------------------------------------------------------------- eight elements of a row
@@ -68,14 +91,25 @@ struct Mat {
   long long ld;
   int dt;
 };
+// The kernels come in two forms.  The typed ones know their operands' types (template arguments
+// ≥ 0) and run on rows of whole 16-byte vectors only; the others take the types from the operands
+// and check every vector, for odd widths, unaligned rows and rarer mixes of types.  The checks and
+// type branches cost about a third of the instructions, which bound these kernels: 8192 x 4096 bf16
+// with a residual, dropout 53.7 us untyped, with LayerNorm 86.5, its backward 133.
+constexpr int ANY = -1;
+template <int DT>
+__device__ __forceinline__ int dt_of(const Mat& t) {
+  if constexpr (DT >= 0) return DT;
+  else return t.dt;
+}
 
 struct Raw8 {
   uint4 a, b;  // 16-bit types: a; fp32: a and b
 };
 
-__device__ __forceinline__ Raw8 load_raw8(const Mat& t, long long row, int c0) {
+__device__ __forceinline__ Raw8 load_raw8(const Mat& t, long long row, int c0, int dt) {
   Raw8 r;
-  if (t.dt == DT_F32) {
+  if (dt == DT_F32) {
     const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(t.p) + row * t.ld + c0);
     r.a = q[0];
     r.b = q[1];
@@ -117,15 +151,16 @@ __device__ __forceinline__ void load_some8(float (&v)[8], const Mat& t, long lon
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = i < cnt ? load1(t.p, row * t.ld + c0 + i, t.dt) : 0.0f;
 }
-__device__ __forceinline__ void store8(const Mat& t, long long row, int c0, int cnt, bool vec, const float (&v)[8]) {
+// v into elements c0 .. c0 + cnt − 1; vec: all eight, as 16-byte stores
+__device__ __forceinline__ void store8(const Mat& t, long long row, int c0, int cnt, bool vec, const float (&v)[8], int dt) {
   if (vec) {
-    if (t.dt == DT_F32) {
+    if (dt == DT_F32) {
       float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(t.p) + row * t.ld + c0);
       q[0] = make_float4(v[0], v[1], v[2], v[3]);
       q[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
       uint4 q;
-      if (t.dt == DT_BF16) {
+      if (dt == DT_BF16) {
         q = make_uint4(pack2<DT_BF16>(v[0], v[1]), pack2<DT_BF16>(v[2], v[3]), pack2<DT_BF16>(v[4], v[5]),
                        pack2<DT_BF16>(v[6], v[7]));
       } else {
@@ -137,7 +172,7 @@ __device__ __forceinline__ void store8(const Mat& t, long long row, int c0, int 
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < cnt) store1(t.p, row * t.ld + c0 + i, t.dt, v[i]);
+      if (i < cnt) store1(t.p, row * t.ld + c0 + i, dt, v[i]);
   }
 }
 // eight parameters of type dt from c0; `dflt` for a null pointer
@@ -147,10 +182,36 @@ __device__ __forceinline__ void load_param8(float (&v)[8], const void* p, int dt
     for (int i = 0; i < 8; ++i) v[i] = dflt;
   } else {
     const Mat t{const_cast<void*>(p), 0, dt};
-    if (vec) widen8(v, load_raw8(t, 0, c0), dt);
+    if (vec) widen8(v, load_raw8(t, 0, c0, dt), dt);
     else load_some8(v, t, 0, c0, cnt);
   }
 }
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 pair_of(const float (&v)[8], int j) { return make_float2(v[2 * j], v[2 * j + 1]); }
+__device__ __forceinline__ void put_pair(float (&v)[8], int j, float2 q) { v[2 * j] = q.x, v[2 * j + 1] = q.y; }
 
 // ---------------------------------------------------------------- dropout
 struct DropoutArgs {
@@ -163,17 +224,21 @@ struct DropoutArgs {
 // Thread i of the grid takes vectors i, i + threads, ... of the M·nvec (row, vector) pairs; row
 // and vector advance by the stride's quotient and remainder, so that one division runs per
 // thread.  Two vectors a trip: both vectors' loads are in flight before the first use.
-__global__ void __launch_bounds__(256) fl_dropout_kernel(const DropoutArgs P) {
+template <int XT, int YT>
+__global__ void __launch_bounds__(256, 4) fl_dropout_kernel(const DropoutArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
+  constexpr bool TYPED = XT >= 0;
+  const int xt = dt_of<XT>(P.x), yt = dt_of<YT>(P.y);
   const long long stride = (long long)gridDim.x * blockDim.x;
   const long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long srow = stride / P.nvec;
   const int svec = (int)(stride - srow * P.nvec);
   long long row = i0 / P.nvec;
   int v = (int)(i0 - row * P.nvec);
-  const uint64_t offset = drop_offset(P.d);
+  const DropOffset off = drop_offset(P.d);
   const long long groups = (P.N + 3) / 4;
+  const bool has_r = P.r.p != nullptr;
   while (row < P.M) {
     long long rows[2];
     int c0[2], cnt[2];
@@ -184,11 +249,11 @@ __global__ void __launch_bounds__(256) fl_dropout_kernel(const DropoutArgs P) {
       rows[u] = row;
       live[u] = row < P.M;
       c0[u] = 8 * v;
-      cnt[u] = min(8, P.N - c0[u]);
-      vec[u] = P.vec && cnt[u] == 8;
+      cnt[u] = TYPED ? 8 : min(8, P.N - c0[u]);
+      vec[u] = TYPED || (P.vec && cnt[u] == 8);
       if (live[u] && vec[u]) {
-        rx[u] = load_raw8(P.x, row, c0[u]);
-        if (P.r.p != nullptr) rr[u] = load_raw8(P.r, row, c0[u]);
+        rx[u] = load_raw8(P.x, row, c0[u], xt);
+        if (has_r) rr[u] = load_raw8(P.r, row, c0[u], yt);
       }
       row += srow;
       v += svec;
@@ -197,50 +262,68 @@ __global__ void __launch_bounds__(256) fl_dropout_kernel(const DropoutArgs P) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (!live[u]) continue;
-      float x[8];
-      if (vec[u]) widen8(x, rx[u], P.x.dt);
+      float x[8], r[8];
+      if (vec[u]) widen8(x, rx[u], xt);
       else load_some8(x, P.x, rows[u], c0[u], cnt[u]);
-      if (P.d.on) drop8(x, (uint64_t)(rows[u] * groups + (c0[u] >> 2)), offset, P.d);
-      if (P.r.p != nullptr) {
-        float r[8];
-        if (vec[u]) widen8(r, rr[u], P.r.dt);
-        else load_some8(r, P.r, rows[u], c0[u], cnt[u]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] += r[i];
+      for (int i = 0; i < 8; ++i) r[i] = 0.0f;
+      if (has_r) {
+        if (vec[u]) widen8(r, rr[u], yt);
+        else load_some8(r, P.r, rows[u], c0[u], cnt[u]);
       }
-      store8(P.y, rows[u], c0[u], cnt[u], vec[u], x);
+      if (P.d.on) {
+        add_dropped8(r, x, (uint64_t)(rows[u] * groups + (c0[u] >> 2)), off, P.d);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] += x[i];
+      }
+      store8(P.y, rows[u], c0[u], cnt[u], vec[u], r, yt);
     }
   }
 }
 
 // ---------------------------------------------------------------- sums over a row's threads
-// Sum of (a, b) over the T threads that share a row, the same in every thread: a butterfly in
-// each warp, then the warps' sums in warp order.  `red` holds two sets of T/32 pairs, used in
-// turn (`flip`), so that one barrier a call is enough: a warp writes a set again only after the
-// next call's barrier, which every reader of the set has passed its reads before.
+// Sums of one or two values over the T threads that share a row, the same in every thread: a
+// butterfly in each warp, then the warps' sums in warp order.  `red` holds two sets of T/32
+// pairs, used in turn (`flip`), so that one barrier a call is enough: a warp writes a set again
+// only after the next call's barrier, which every reader of the set has passed its reads before.
 template <int T>
-__device__ __forceinline__ float2 row_sum(float a, float b, float2* red, int& flip, int group) {
+__device__ __forceinline__ float2 row_sum2(float2 v, float2* red, int& flip, int group) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
+  for (int o = 16; o > 0; o >>= 1)
+    v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
   if constexpr (T > 32) {
     constexpr int W = T / 32;
     float2* set = red + flip * W;
     flip ^= 1;
-    const int w = (threadIdx.x % T) >> 5;
-    if ((threadIdx.x & 31) == 0) set[w] = make_float2(a, b);
+    if ((threadIdx.x & 31) == 0) set[(threadIdx.x % T) >> 5] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(T) : "memory");
-    a = b = 0.0f;
+    v = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float2 q = set[i];
-      a += q.x;
-      b += q.y;
+    for (int i = 0; i < W; i += 2) {
+      const float4 q = *reinterpret_cast<const float4*>(set + i);
+      v = add2(v, make_float2(q.x, q.y));
+      v = add2(v, make_float2(q.z, q.w));
     }
   }
-  return make_float2(a, b);
+  return v;
+}
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float2* red2, int& flip, int group) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (T > 32) {
+    constexpr int W = T / 32;
+    float* set = reinterpret_cast<float*>(red2 + flip * W);
+    flip ^= 1;
+    if ((threadIdx.x & 31) == 0) set[(threadIdx.x % T) >> 5] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(T) : "memory");
+    float2 a = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < W; i += 2) a = add2(a, *reinterpret_cast<const float2*>(set + i));
+    v = a.x + a.y;
+  }
+  return v;
 }
 
 // ---------------------------------------------------------------- rows ahead in shared memory
@@ -259,11 +342,11 @@ __host__ __device__ __forceinline__ uint32_t operand_bytes(const Mat& t, int v, 
   return t.p == nullptr ? 0u : plane_bytes(v, block) * (t.dt == DT_F32 ? 2u : 1u);
 }
 template <int V, int BLOCK>
-__device__ __forceinline__ void stage_vec(uint32_t dst, const Mat& t, long long row, int c0, int k) {
-  const char* src = reinterpret_cast<const char*>(t.p) + (row * t.ld + c0) * (t.dt == DT_F32 ? 4 : 2);
+__device__ __forceinline__ void stage_vec(uint32_t dst, const Mat& t, long long row, int c0, int k, int dt) {
+  const char* src = reinterpret_cast<const char*>(t.p) + (row * t.ld + c0) * (dt == DT_F32 ? 4 : 2);
   const uint32_t a = dst + (uint32_t)(k * BLOCK + threadIdx.x) * 16u;
   cp_async_16(a, src, 16u);
-  if (t.dt == DT_F32) cp_async_16(a + plane_bytes(V, BLOCK), src + 16, 16u);
+  if (dt == DT_F32) cp_async_16(a + plane_bytes(V, BLOCK), src + 16, 16u);
 }
 template <int V, int BLOCK>
 __device__ __forceinline__ void unstage_vec(float (&v)[8], uint32_t src, int dt, int k) {
@@ -293,88 +376,121 @@ struct DropLnArgs {
 
 // T threads hold a row, V vectors of eight each (N ≤ 8·V·T): the row is read once, stays in
 // registers through the mean, Σ(s − μ)² and the normalisation, and every output is written once.
-// A CTA holds max(1, 128/T) rows at a time and walks the rows a grid apart.
-template <int T, int V>
-__global__ void __launch_bounds__(T < 128 ? 128 : T) fl_dropout_ln_kernel(const DropLnArgs P) {
+// A CTA holds max(1, 128/T) rows at a time and walks the rows a grid apart; γ and β stay in
+// registers (but for 1024 threads, which have 64 each).
+__host__ __device__ constexpr int ln_block(int t) { return t < 128 ? 128 : t; }
+template <int T, int V, int XT, int ST, int ZT>
+__global__ void __launch_bounds__(ln_block(T), T <= 128 ? 6 : T == 256 ? 3 : 1) fl_dropout_ln_kernel(const DropLnArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
-  constexpr int BLOCK = T < 128 ? 128 : T;
+  constexpr bool TYPED = XT >= 0, HOIST = T < 1024;
+  constexpr int BLOCK = ln_block(T);
   constexpr int R = BLOCK / T;
   extern __shared__ __align__(16) uint8_t ring_s[];
-  __shared__ float2 red_s[R][2 * (T / 32)];
+  __shared__ __align__(16) float2 red_s[R][2 * (T / 32)];
+  const int xt = dt_of<XT>(P.x), st = ST >= 0 ? ST : (P.r.p != nullptr ? P.r.dt : P.s.dt), zt = dt_of<ZT>(P.z);
   const int group = threadIdx.x / T, t = threadIdx.x % T;
   int flip = 0;
-  const uint64_t offset = drop_offset(P.d);
+  const DropOffset off = drop_offset(P.d);
   const long long groups = (P.N + 3) / 4;
   const float n_f = (float)P.N;
   const long long m0 = (long long)blockIdx.x * R + group, step = (long long)gridDim.x * R;
   const uint32_t ring = smem_u32(ring_s);
   const uint32_t xb = operand_bytes(P.x, V, BLOCK), slot_bytes = xb + operand_bytes(P.r, V, BLOCK);
+  const bool has_r = P.r.p != nullptr;
+  // elements of vector k inside the row (typed: 8 or none)
+  auto count = [&](int k) {
+    const int left = P.N - 8 * (k * T + t);
+    return TYPED ? (left > 0 ? 8 : 0) : max(0, min(8, left));
+  };
   auto prefetch = [&](long long m, uint32_t slot) {
-    if (m < P.M && P.vec) {
+    if (m < P.M && (TYPED || P.vec)) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int c0 = 8 * (k * T + t);
-        if (c0 + 8 <= P.N) {
-          stage_vec<V, BLOCK>(slot, P.x, m, c0, k);
-          if (P.r.p != nullptr) stage_vec<V, BLOCK>(slot + xb, P.r, m, c0, k);
+        if (count(k) == 8) {
+          stage_vec<V, BLOCK>(slot, P.x, m, c0, k, xt);
+          if (has_r) stage_vec<V, BLOCK>(slot + xb, P.r, m, c0, k, st);
         }
       }
     }
     cp_async_commit();
   };
   for (int i = 0; i < P.ahead; ++i) prefetch(m0 + i * step, ring + i * slot_bytes);
+  float gam[HOIST ? V : 1][8], bet[HOIST ? V : 1][8];
+  auto params = [&](int k, float (&g)[8], float (&b)[8]) {
+    const int c0 = 8 * (k * T + t), cnt = count(k);
+    const bool vec = TYPED || (P.vec && cnt == 8);
+    load_param8(g, P.gamma, P.param_dt, c0, cnt, vec, 1.0f);
+    load_param8(b, P.beta, P.param_dt, c0, cnt, vec, 0.0f);
+  };
+  if constexpr (HOIST) {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (count(k) > 0) params(k, gam[k], bet[k]);
+  }
   int at = 0;
   for (long long m = m0; m < P.M; m += step) {
     const uint32_t slot = ring + at * slot_bytes;
     float s[V][8];
-    float sum = 0.0f;
+    float2 sum2 = make_float2(0.0f, 0.0f);
     wait_row(P.ahead);  // this row's copies have landed
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c0 = 8 * (k * T + t);
-      const int cnt = max(0, min(8, P.N - c0));
-      const bool vec = P.vec && cnt == 8;
-      if (vec) unstage_vec<V, BLOCK>(s[k], slot, P.x.dt, k);
-      else load_some8(s[k], P.x, m, c0, cnt);
+      const int c0 = 8 * (k * T + t), cnt = count(k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[k][i] = 0.0f;
       if (cnt == 0) continue;
-      if (P.d.on) drop8(s[k], (uint64_t)(m * groups + (c0 >> 2)), offset, P.d);
-      if (P.r.p != nullptr) {
-        float r[8];
-        if (vec) unstage_vec<V, BLOCK>(r, slot + xb, P.r.dt, k);
-        else load_some8(r, P.r, m, c0, cnt);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[k][i] += r[i];
+      const bool vec = TYPED || (P.vec && cnt == 8);
+      float x[8];
+      if (vec) unstage_vec<V, BLOCK>(x, slot, xt, k);
+      else load_some8(x, P.x, m, c0, cnt);
+      if (has_r) {
+        if (vec) unstage_vec<V, BLOCK>(s[k], slot + xb, st, k);
+        else load_some8(s[k], P.r, m, c0, cnt);
       }
-      if (P.s.p != nullptr) store8(P.s, m, c0, cnt, vec, s[k]);
+      if (P.d.on) {
+        add_dropped8(s[k], x, (uint64_t)(m * groups + (c0 >> 2)), off, P.d);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += i < cnt ? s[k][i] : 0.0f;
+        for (int j = 0; j < 4; ++j) put_pair(s[k], j, add2(pair_of(s[k], j), pair_of(x, j)));
+      }
+      if (P.s.p != nullptr) store8(P.s, m, c0, cnt, vec, s[k], st);
+      // (elements past the row were loaded as zeros, and zeros they stay)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum2 = add2(sum2, pair_of(s[k], j));
     }
     prefetch(m + P.ahead * step, slot);  // (the slot's values are in registers)
     at = at + 1 == P.ahead ? 0 : at + 1;
-    const float mean = row_sum<T>(sum, 0.0f, red_s[group], flip, group).x / n_f;
-    float q = 0.0f;
+    const float mean = row_sum<T>(sum2.x + sum2.y, red_s[group], flip, group) / n_f;
+    float2 q2 = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int cnt = P.N - 8 * (k * T + t);
+      const int cnt = count(k);
+      if (cnt == 0) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q += i < cnt ? (s[k][i] - mean) * (s[k][i] - mean) : 0.0f;
+      for (int j = 0; j < 4; ++j) {
+        float2 d = add2(pair_of(s[k], j), make_float2(-mean, -mean));
+        if (!TYPED) d = make_float2(2 * j < cnt ? d.x : 0.0f, 2 * j + 1 < cnt ? d.y : 0.0f);
+        put_pair(s[k], j, d);  // from here on s − μ
+        q2 = fma2(d, d, q2);
+      }
     }
-    const float var = row_sum<T>(q, 0.0f, red_s[group], flip, group).x / n_f;
-    const float rstd = 1.0f / sqrtf(var + P.eps);
+    const float rstd = 1.0f / sqrtf(row_sum<T>(q2.x + q2.y, red_s[group], flip, group) / n_f + P.eps);
     if (t == 0 && P.mean != nullptr) P.mean[m] = mean, P.rstd[m] = rstd;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c0 = 8 * (k * T + t);
-      const int cnt = min(8, P.N - c0);
-      if (cnt <= 0) continue;
-      const bool vec = P.vec && cnt == 8;
+      const int c0 = 8 * (k * T + t), cnt = count(k);
+      if (cnt == 0) continue;
       float g[8], b[8];
-      load_param8(g, P.gamma, P.param_dt, c0, cnt, vec, 1.0f);
-      load_param8(b, P.beta, P.param_dt, c0, cnt, vec, 0.0f);
+      if constexpr (!HOIST) params(k, g, b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = (s[k][i] - mean) * rstd * g[i] + b[i];
-      store8(P.z, m, c0, cnt, vec, g);
+      for (int j = 0; j < 4; ++j) {
+        const float2 u = mul2(pair_of(s[k], j), make_float2(rstd, rstd));
+        put_pair(s[k], j, HOIST ? fma2(u, pair_of(gam[HOIST ? k : 0], j), pair_of(bet[HOIST ? k : 0], j))
+                                : fma2(u, pair_of(g, j), pair_of(b, j)));
+      }
+      store8(P.z, m, c0, cnt, TYPED || (P.vec && cnt == 8), s[k], zt);
     }
   }
   cp_async_wait<0>();  // no copy is in flight when the CTA leaves
@@ -386,22 +502,27 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) fl_dropout_ln_kernel(const 
 __global__ void __launch_bounds__(1024) fl_dropout_ln_long_kernel(const DropLnArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
-  __shared__ float2 red[2 * 32];
+  __shared__ __align__(16) float2 red[2 * 32];
   int flip = 0;
-  const uint64_t offset = drop_offset(P.d);
+  const DropOffset off = drop_offset(P.d);
   const long long groups = (P.N + 3) / 4;
   const float n_f = (float)P.N;
   for (long long m = blockIdx.x; m < P.M; m += gridDim.x) {
     auto value = [&](int c0, int cnt, bool vec, float (&s)[8]) {
-      if (vec) widen8(s, load_raw8(P.x, m, c0), P.x.dt);
-      else load_some8(s, P.x, m, c0, cnt);
-      if (P.d.on) drop8(s, (uint64_t)(m * groups + (c0 >> 2)), offset, P.d);
-      if (P.r.p != nullptr) {
-        float r[8];
-        if (vec) widen8(r, load_raw8(P.r, m, c0), P.r.dt);
-        else load_some8(r, P.r, m, c0, cnt);
+      float x[8];
+      if (vec) widen8(x, load_raw8(P.x, m, c0, P.x.dt), P.x.dt);
+      else load_some8(x, P.x, m, c0, cnt);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] += r[i];
+      for (int i = 0; i < 8; ++i) s[i] = 0.0f;
+      if (P.r.p != nullptr) {
+        if (vec) widen8(s, load_raw8(P.r, m, c0, P.r.dt), P.r.dt);
+        else load_some8(s, P.r, m, c0, cnt);
+      }
+      if (P.d.on) {
+        add_dropped8(s, x, (uint64_t)(m * groups + (c0 >> 2)), off, P.d);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += x[i];
       }
     };
     float mean = 0.0f, rstd = 0.0f;
@@ -425,12 +546,12 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_long_kernel(const DropLnAr
           load_param8(b, P.beta, P.param_dt, c0, cnt, vec, 0.0f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] = (s[i] - mean) * rstd * g[i] + b[i];
-          if (P.s.p != nullptr) store8(P.s, m, c0, cnt, vec, s);
-          store8(P.z, m, c0, cnt, vec, g);
+          if (P.s.p != nullptr) store8(P.s, m, c0, cnt, vec, s, P.s.dt);
+          store8(P.z, m, c0, cnt, vec, g, P.z.dt);
         }
       }
-      if (step == 0) mean = row_sum<1024>(acc, 0.0f, red, flip, 0).x / n_f;
-      if (step == 1) rstd = 1.0f / sqrtf(row_sum<1024>(acc, 0.0f, red, flip, 0).x / n_f + P.eps);
+      if (step == 0) mean = row_sum<1024>(acc, red, flip, 0) / n_f;
+      if (step == 1) rstd = 1.0f / sqrtf(row_sum<1024>(acc, red, flip, 0) / n_f + P.eps);
     }
     if (threadIdx.x == 0 && P.mean != nullptr) P.mean[m] = mean, P.rstd[m] = rstd;
   }
@@ -448,109 +569,134 @@ struct DropLnBwdArgs {
 };
 
 // With u = (s − μ)·rstd and g = dz·γ:  ds = rstd·(g − mean(g) − u·mean(g·u)) + ds_in,
-// dx = D(ds), dγ = Σ_m dz·u, dβ = Σ_m dz.  T threads share a row, V vectors each, staged two rows
-// ahead in shared memory and read from there twice (for the sums, then for the gradients), so that
+// dx = D(ds), dγ = Σ_m dz·u, dβ = Σ_m dz.  T threads share a row, V vectors each, staged rows
+// ahead in shared memory (V > 1: read from there twice, for the sums and for the gradients), so that
 // registers hold little beside the dγ, dβ sums of the thread's columns, which it keeps over all its
 // rows.  A CTA of 512 (or T) threads holds R rows at a time; at the end its row groups add their
 // sums in turn in shared memory and store one partial row each of dγ and dβ, which
 // fl_ln_wgrad_kernel adds in a fixed order.
-template <int T, int V>
-__global__ void __launch_bounds__(T < 512 ? 512 : T, T < 1024 ? 2 : 1) fl_dropout_ln_bwd_kernel(const DropLnBwdArgs P) {
+__host__ __device__ constexpr int ln_bwd_block(int t) { return t < 512 ? 512 : t; }
+template <int T, int V, int XT, int ST, int ZT>
+__global__ void __launch_bounds__(ln_bwd_block(T), T < 1024 ? 2 : 1) fl_dropout_ln_bwd_kernel(const DropLnBwdArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
-  constexpr int BLOCK = T < 512 ? 512 : T;
+  constexpr bool TYPED = XT >= 0;
+  constexpr int BLOCK = ln_bwd_block(T);
   constexpr int R = BLOCK / T;
   extern __shared__ __align__(16) uint8_t ring_s[];
-  __shared__ float2 red_s[R][2 * (T / 32)];
+  __shared__ __align__(16) float2 red_s[R][2 * (T / 32)];
   __shared__ float part_s[R > 1 ? 16 * V * T : 1];
+  const int xt = dt_of<XT>(P.dx), st = dt_of<ST>(P.s), zt = dt_of<ZT>(P.dz);
   const int group = threadIdx.x / T, t = threadIdx.x % T;
   int flip = 0;
-  const uint64_t offset = drop_offset(P.d);
+  const DropOffset off = drop_offset(P.d);
   const long long groups = (P.N + 3) / 4;
   const float n_f = (float)P.N;
   const long long m0 = (long long)blockIdx.x * R + group, step = (long long)gridDim.x * R;
   const uint32_t ring = smem_u32(ring_s);
   const uint32_t zb = operand_bytes(P.dz, V, BLOCK), sb = operand_bytes(P.s, V, BLOCK);
   const uint32_t slot_bytes = zb + sb + operand_bytes(P.ds_in, V, BLOCK);
-  float pg[V][8], pb[V][8];
-#pragma unroll
-  for (int k = 0; k < V; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) pg[k][i] = pb[k][i] = 0.0f;
+  const bool has_in = P.ds_in.p != nullptr;
+  auto count = [&](int k) {
+    const int left = P.N - 8 * (k * T + t);
+    return TYPED ? (left > 0 ? 8 : 0) : max(0, min(8, left));
+  };
   auto prefetch = [&](long long m, uint32_t slot) {
-    if (m < P.M && P.vec) {
+    if (m < P.M && (TYPED || P.vec)) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int c0 = 8 * (k * T + t);
-        if (c0 + 8 <= P.N) {
-          stage_vec<V, BLOCK>(slot, P.dz, m, c0, k);
-          stage_vec<V, BLOCK>(slot + zb, P.s, m, c0, k);
-          if (P.ds_in.p != nullptr) stage_vec<V, BLOCK>(slot + zb + sb, P.ds_in, m, c0, k);
+        if (count(k) == 8) {
+          stage_vec<V, BLOCK>(slot, P.dz, m, c0, k, zt);
+          stage_vec<V, BLOCK>(slot + zb, P.s, m, c0, k, st);
+          if (has_in) stage_vec<V, BLOCK>(slot + zb + sb, P.ds_in, m, c0, k, st);
         }
       }
     }
     cp_async_commit();
   };
   for (int i = 0; i < P.ahead; ++i) prefetch(m0 + i * step, ring + i * slot_bytes);
+  float pg[V][8], pb[V][8];
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pg[k][i] = pb[k][i] = 0.0f;
+  auto param = [&](int k, float (&g)[8]) {
+    const int cnt = count(k);
+    load_param8(g, P.gamma, P.param_dt, 8 * (k * T + t), cnt, TYPED || (P.vec && cnt == 8), 1.0f);
+  };
+  float gam[8];
+  if (V == 1 && count(0) > 0) param(0, gam);
   int at = 0;
   for (long long m = m0; m < P.M; m += step) {
     const uint32_t slot = ring + at * slot_bytes;
     const float mean = P.mean[m], rstd = P.rstd[m];
     // dz and u = (s − μ)·rstd of vector k (zeros past N)
-    auto values = [&](int k, int c0, int cnt, bool vec, float (&dz)[8], float (&u)[8]) {
-      if (vec) {
-        unstage_vec<V, BLOCK>(dz, slot, P.dz.dt, k);
-        unstage_vec<V, BLOCK>(u, slot + zb, P.s.dt, k);
+    auto values = [&](int k, int cnt, float (&dz)[8], float (&u)[8]) {
+      if (TYPED || (P.vec && cnt == 8)) {
+        unstage_vec<V, BLOCK>(dz, slot, zt, k);
+        unstage_vec<V, BLOCK>(u, slot + zb, st, k);
       } else {
-        load_some8(dz, P.dz, m, c0, cnt);
-        load_some8(u, P.s, m, c0, cnt);
+        load_some8(dz, P.dz, m, 8 * (k * T + t), cnt);
+        load_some8(u, P.s, m, 8 * (k * T + t), cnt);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = i < cnt ? (u[i] - mean) * rstd : 0.0f;
+      for (int j = 0; j < 4; ++j) {
+        float2 q = mul2(add2(pair_of(u, j), make_float2(-mean, -mean)), make_float2(rstd, rstd));
+        if (!TYPED) q = make_float2(2 * j < cnt ? q.x : 0.0f, 2 * j + 1 < cnt ? q.y : 0.0f);
+        put_pair(u, j, q);
+      }
     };
     wait_row(P.ahead);
-    float a = 0.0f, b = 0.0f;
+    float2 a2 = make_float2(0.0f, 0.0f), b2 = a2;
+    float g[8], u[8];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c0 = 8 * (k * T + t);
-      const int cnt = min(8, P.N - c0);
-      if (cnt <= 0) continue;
-      const bool vec = P.vec && cnt == 8;
-      float dz[8], u[8], gam[8];
-      load_param8(gam, P.gamma, P.param_dt, c0, cnt, vec, 1.0f);
-      values(k, c0, cnt, vec, dz, u);
+      const int cnt = count(k);
+      if (cnt == 0) continue;
+      values(k, cnt, g, u);
+      if constexpr (V > 1) param(k, gam);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        pg[k][i] = fmaf(dz[i], u[i], pg[k][i]);
-        pb[k][i] += dz[i];
-        const float g = dz[i] * gam[i];
-        a += i < cnt ? g : 0.0f;
-        b = fmaf(g, u[i], b);
+      for (int j = 0; j < 4; ++j) {
+        const float2 z = pair_of(g, j), w = pair_of(u, j);
+        put_pair(pg[k], j, fma2(z, w, pair_of(pg[k], j)));
+        put_pair(pb[k], j, add2(z, pair_of(pb[k], j)));
+        // (past the row dz is 0; a γ read there is not: only dz·γ enters the sums)
+        float2 q = mul2(z, pair_of(gam, j));
+        put_pair(g, j, q);
+        a2 = add2(a2, q);
+        b2 = fma2(q, w, b2);
       }
     }
-    const float2 ab = row_sum<T>(a, b, red_s[group], flip, group);
+    const float2 ab = row_sum2<T>(make_float2(a2.x + a2.y, b2.x + b2.y), red_s[group], flip, group);
     const float ma = ab.x / n_f, mb = ab.y / n_f;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c0 = 8 * (k * T + t);
-      const int cnt = min(8, P.N - c0);
-      if (cnt <= 0) continue;
-      const bool vec = P.vec && cnt == 8;
-      float dz[8], u[8], gam[8];
-      load_param8(gam, P.gamma, P.param_dt, c0, cnt, vec, 1.0f);
-      values(k, c0, cnt, vec, dz, u);
+      const int c0 = 8 * (k * T + t), cnt = count(k);
+      if (cnt == 0) continue;
+      const bool vec = TYPED || (P.vec && cnt == 8);
+      if constexpr (V > 1) {
+        values(k, cnt, g, u);
+        param(k, gam);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dz[i] = rstd * (dz[i] * gam[i] - ma - u[i] * mb);
-      if (P.ds_in.p != nullptr) {
-        if (vec) unstage_vec<V, BLOCK>(u, slot + zb + sb, P.ds_in.dt, k);
-        else load_some8(u, P.ds_in, m, c0, cnt);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dz[i] += u[i];
+        for (int j = 0; j < 4; ++j) put_pair(g, j, mul2(pair_of(g, j), pair_of(gam, j)));
       }
-      if (P.dres.p != nullptr) store8(P.dres, m, c0, cnt, vec, dz);
+      float in[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) in[i] = 0.0f;
+      if (has_in) {
+        if (vec) unstage_vec<V, BLOCK>(in, slot + zb + sb, st, k);
+        else load_some8(in, P.ds_in, m, c0, cnt);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 q = fma2(pair_of(u, j), make_float2(-mb, -mb), add2(pair_of(g, j), make_float2(-ma, -ma)));
+        put_pair(in, j, fma2(q, make_float2(rstd, rstd), pair_of(in, j)));
+      }
+      if (P.dres.p != nullptr) store8(P.dres, m, c0, cnt, vec, in, st);
       if (P.dx.p != nullptr) {
-        if (P.d.on) drop8(dz, (uint64_t)(m * groups + (c0 >> 2)), offset, P.d);
-        store8(P.dx, m, c0, cnt, vec, dz);
+        if (P.d.on) drop8(in, (uint64_t)(m * groups + (c0 >> 2)), off, P.d);
+        store8(P.dx, m, c0, cnt, vec, in, xt);
       }
     }
     prefetch(m + P.ahead * step, slot);
@@ -561,14 +707,14 @@ __global__ void __launch_bounds__(T < 512 ? 512 : T, T < 1024 ? 2 : 1) fl_dropou
   float* out = P.ws + (long long)blockIdx.x * 2 * P.ws_ld;
   if constexpr (R > 1) {
     constexpr int W = 8 * V * T;
-    for (int g = 0; g < R; ++g) {
-      if (group == g) {
+    for (int gr = 0; gr < R; ++gr) {
+      if (group == gr) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int c = (i * V + k) * T + t;  // (a warp's lanes side by side: no bank conflicts)
-            if (g > 0) pg[k][i] += part_s[c], pb[k][i] += part_s[W + c];
+            if (gr > 0) pg[k][i] += part_s[c], pb[k][i] += part_s[W + c];
             part_s[c] = pg[k][i];
             part_s[W + c] = pb[k][i];
           }
@@ -597,9 +743,9 @@ __global__ void __launch_bounds__(T < 512 ? 512 : T, T < 1024 ? 2 : 1) fl_dropou
 __global__ void __launch_bounds__(1024) fl_dropout_ln_bwd_long_kernel(const DropLnBwdArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
-  __shared__ float2 red[2 * 32];
+  __shared__ __align__(16) float2 red[2 * 32];
   int flip = 0;
-  const uint64_t offset = drop_offset(P.d);
+  const DropOffset off = drop_offset(P.d);
   const long long groups = (P.N + 3) / 4;
   const float n_f = (float)P.N;
   float* out = P.ws == nullptr ? nullptr : P.ws + (long long)blockIdx.x * 2 * P.ws_ld;
@@ -615,8 +761,8 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_bwd_long_kernel(const Drop
         const bool vec = P.vec && cnt == 8;
         float dz[8], u[8], gam[8];
         if (vec) {
-          widen8(dz, load_raw8(P.dz, m, c0), P.dz.dt);
-          widen8(u, load_raw8(P.s, m, c0), P.s.dt);
+          widen8(dz, load_raw8(P.dz, m, c0, P.dz.dt), P.dz.dt);
+          widen8(u, load_raw8(P.s, m, c0, P.s.dt), P.s.dt);
         } else {
           load_some8(dz, P.dz, m, c0, cnt);
           load_some8(u, P.s, m, c0, cnt);
@@ -642,20 +788,20 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_bwd_long_kernel(const Drop
           for (int i = 0; i < 8; ++i) dz[i] = rstd * (dz[i] * gam[i] - ma - u[i] * mb);
           if (P.ds_in.p != nullptr) {
             float in[8];
-            if (vec) widen8(in, load_raw8(P.ds_in, m, c0), P.ds_in.dt);
+            if (vec) widen8(in, load_raw8(P.ds_in, m, c0, P.ds_in.dt), P.ds_in.dt);
             else load_some8(in, P.ds_in, m, c0, cnt);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dz[i] += in[i];
           }
-          if (P.dres.p != nullptr) store8(P.dres, m, c0, cnt, vec, dz);
+          if (P.dres.p != nullptr) store8(P.dres, m, c0, cnt, vec, dz, P.dres.dt);
           if (P.dx.p != nullptr) {
-            if (P.d.on) drop8(dz, (uint64_t)(m * groups + (c0 >> 2)), offset, P.d);
-            store8(P.dx, m, c0, cnt, vec, dz);
+            if (P.d.on) drop8(dz, (uint64_t)(m * groups + (c0 >> 2)), off, P.d);
+            store8(P.dx, m, c0, cnt, vec, dz, P.dx.dt);
           }
         }
       }
       if (step == 0) {
-        const float2 ab = row_sum<1024>(a, b, red, flip, 0);
+        const float2 ab = row_sum2<1024>(make_float2(a, b), red, flip, 0);
         ma = ab.x / n_f;
         mb = ab.y / n_f;
       }
