@@ -24,6 +24,7 @@ _GEMM = ["fl_gemm.cuh", "fl_ptx.cuh", "fl_host.h"]
 UNITS = {
     "fl_api.cu": ["fl_elementwise.cuh", "fl_plan.h", *_GEMM],
     "fl_pair.cu": ["fl_pair.cuh", "fl_plan.h", *_GEMM],
+    "fl_small.cu": ["fl_small.cuh", "fl_pair.cuh", "fl_plan.h", *_GEMM],
     "fl_rows.cu": ["fl_rows.cuh", *_GEMM],
 }
 HEADER = os.path.join(ROOT, "include", "fused_linear.h")

@@ -687,7 +687,7 @@ extern "C" fl_status fl_plan_preview(int64_t M, int64_t N, int64_t K, int32_t dt
 extern "C" fl_status fl_get_plan_info(fl_plan_t p, fl_plan_info* info) {
   if (!p || !info) return fail(FL_ERR_INVALID_ARG, "fl_get_plan_info: null argument");
   memset(info, 0, sizeof(*info));
-  info->tile_m = p->swap ? p->mma_n : (p->pair ? 256 : 128);
+  info->tile_m = p->swap || p->small ? p->mma_n : (p->pair ? 256 : 128);
   info->tile_n = p->swap ? 128 : p->out_tile_n;
   info->mma_n = p->mma_n;
   info->swap_ab = p->swap ? 1 : 0;

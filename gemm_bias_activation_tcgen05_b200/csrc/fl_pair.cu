@@ -79,6 +79,11 @@ fl_status fl::host::pair_config(fl_plan_s* p, bool no_workspace) {
   const bool glu = epi == EPI_GLU || epi == EPI_GLU_AUX;
   const int64_t P = std::max(1, p->num_sms / 2);
   p->swap = false;
+  p->small = false;
+  if (epi == EPI_GLU && p->M <= small_max_rows()) {
+    small_config(p);
+    return FL_OK;
+  }
   p->pair = true;
   p->k_atoms = 1;
   p->num_kb = (int)cdiv(p->K, kPairBk);
@@ -117,6 +122,7 @@ fl_status fl::host::pair_config(fl_plan_s* p, bool no_workspace) {
 }
 
 fl_status fl::host::pair_prepare(const fl_plan_s* p) {
+  if (p->small) return FL_OK;
   FL_CUDA(cudaFuncSetAttribute(p->kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p->max_smem));
   return FL_OK;
 }
@@ -127,9 +133,9 @@ size_t fl::host::pair_workspace_bytes(const fl_plan_s* p) {
 
 fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, void* aux, const void* residual, void* out,
                                  cudaStream_t stream) {
+  if (p->small) return small_execute(p, A, W, out, stream);
   const fl_epilogue_desc& e = p->epi;
   const int epi = epi_of(e.kind);
-  const bool glu = epi == EPI_GLU || epi == EPI_GLU_AUX;
   const bool split = p->split_k > 1;
   const int kout = kernel_out(p);
   const uint64_t es = 2, eo = (uint64_t)esize(e.out_dtype);
@@ -211,7 +217,6 @@ fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, voi
     }
     if (st) return st;
   }
-  (void)glu;
 
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)p->grid, 1, 1);

@@ -505,7 +505,7 @@ struct GradReduceArgs {
   int N, nvec;
   float scale;
 };
-__global__ void __launch_bounds__(256) fl_grad_reduce_kernel(const GradReduceArgs P) {
+static __global__ void __launch_bounds__(256) fl_grad_reduce_kernel(const GradReduceArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   const long long total = P.M * P.nvec;

@@ -27,6 +27,7 @@ struct fl_plan_s {
   // configuration
   bool swap;
   bool pair;  // two CTAs share one 256-row UMMA tile (cluster of 2)
+  bool small;  // the gated linear unit of a few rows (fl_small.cuh)
   int k_atoms;  // 128-byte K atoms per pipeline stage
   int mma_n, out_tile_n, split_k, stages, grid, smem;
   int tiles_a, tiles_b, num_kb;
@@ -66,6 +67,11 @@ fl_status pair_prepare(const fl_plan_s* p);
 size_t pair_workspace_bytes(const fl_plan_s* p);
 fl_status pair_execute(fl_plan_s* p, const void* A, const void* W, void* aux, const void* residual, void* out,
                        cudaStream_t stream);
+
+// The gated linear unit of a few rows: most rows it takes, its configuration and its launch.
+int small_max_rows();
+void small_config(fl_plan_s* p);
+fl_status small_execute(const fl_plan_s* p, const void* A, const void* W, void* out, cudaStream_t stream);
 
 }  // namespace host
 }  // namespace fl

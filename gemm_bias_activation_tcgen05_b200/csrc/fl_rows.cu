@@ -80,8 +80,9 @@ struct RowKernel {
 // The types that have kernels of their own: activations in one 16-bit type, with the residual
 // stream in the same type or in fp32.  Everything else runs on the untyped kernels.
 enum RowTypes { ROWS_ANY, ROWS_BF16, ROWS_F16, ROWS_BF16_F32, ROWS_F16_F32 };
-RowTypes row_types(bool whole_vectors, int x, int s, int z) {
-  if (!whole_vectors || x != z || x == FL_F32) return ROWS_ANY;
+RowTypes row_types(bool vec, int64_t M, int64_t N, int x, int s, int z) {
+  // (the typed kernels count blocks of random numbers in 32 bits)
+  if (!vec || N % 8 != 0 || M * (N / 4) >= (1LL << 32) || x != z || x == FL_F32) return ROWS_ANY;
   if (s == x) return x == FL_BF16 ? ROWS_BF16 : ROWS_F16;
   if (s == FL_F32) return x == FL_BF16 ? ROWS_BF16_F32 : ROWS_F16_F32;
   return ROWS_ANY;
@@ -117,21 +118,21 @@ RowKernel<DropLnArgs> ln_kernel(int64_t N, RowTypes r) {
   if (N <= 16384) return ln_of<1024, 2>(r);
   return {fl_dropout_ln_long_kernel, 0, 0, 1024};
 }
-// Backward: one vector a thread as far as a CTA goes, since the column sums stay in registers.
+// Backward: two vectors a thread, which measured 85.8 us on 8192 x 4096 bf16 against 99.4 for one
+// (and twice the threads): what a row costs beside its elements is spread over more of them.
 RowKernel<DropLnBwdArgs> ln_bwd_kernel(int64_t N, RowTypes r) {
-  if (N <= 256) return ln_bwd_of<32, 1>(r);
-  if (N <= 512) return ln_bwd_of<64, 1>(r);
-  if (N <= 1024) return ln_bwd_of<128, 1>(r);
-  if (N <= 2048) return ln_bwd_of<256, 1>(r);
-  if (N <= 4096) return ln_bwd_of<512, 1>(r);
-  if (N <= 8192) return ln_bwd_of<1024, 1>(r);
+  if (N <= 512) return ln_bwd_of<32, 2>(r);
+  if (N <= 1024) return ln_bwd_of<64, 2>(r);
+  if (N <= 2048) return ln_bwd_of<128, 2>(r);
+  if (N <= 4096) return ln_bwd_of<256, 2>(r);
+  if (N <= 8192) return ln_bwd_of<512, 2>(r);
   if (N <= 16384) return ln_bwd_of<1024, 2>(r);
   return {fl_dropout_ln_bwd_long_kernel, 0, 0, 1024};
 }
 
 // Launch geometry of the backward pass: CTAs (each leaves one partial row of dγ and one of dβ)
-// and the pitch of those rows.  At most two CTAs per SM (one of 1024 threads), the residency the
-// kernel is built for: more would only add partial rows.
+// and the pitch of those rows.  At most two CTAs per SM (one of 512 threads or more), the
+// residency the kernel is built for: more would only add partial rows.
 struct BwdGeom {
   RowKernel<DropLnBwdArgs> k;
   int grid, ws_ld;
@@ -141,20 +142,21 @@ BwdGeom bwd_geom(int64_t M, int64_t N, int sms, RowTypes r) {
   BwdGeom g;
   g.k = ln_bwd_kernel(N, r);
   const int64_t ctas = cdiv(M, g.k.threads == 0 ? 1 : g.k.block / g.k.threads);
-  g.grid = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)sms * (g.k.block == 1024 ? 1 : 2)));
+  g.grid = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)sms * (g.k.block >= 512 ? 1 : 2)));
   g.ws_ld = (int)(cdiv(N, 8) * 8);
   g.bytes = (size_t)g.grid * 2 * (size_t)g.ws_ld * sizeof(float);
   return g;
 }
 
 // The ring of rows ahead: two slots of `slot` bytes, or one where two do not fit, or none for
-// rows that are read in place.  A ring that takes a CTA above 48 KB with the kernel's own arrays
+// rows that are read in place (but at least `least` bytes).  A ring that takes a CTA above 48 KB with the kernel's own arrays
 // needs the kernel's opt-in.
 template <typename Args>
-fl_status ring_of(const RowKernel<Args>& k, size_t slot, Args* P, size_t* smem) {
+fl_status ring_of(const RowKernel<Args>& k, size_t slot, size_t least, Args* P, size_t* smem) {
   constexpr size_t kMost = 200 * 1024;  // of the 227 KB of a CTA; the kernels' own arrays take at most 17 KB
   P->ahead = kRowsAhead * slot <= kMost ? kRowsAhead : 1;
   *smem = k.threads == 0 || !P->vec ? 0 : P->ahead * slot;
+  *smem = std::max(*smem, least);
   if (*smem > 24 * 1024)
     FL_CUDA(cudaFuncSetAttribute((const void*)k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost));
   return FL_OK;
@@ -185,9 +187,10 @@ extern "C" fl_status fl_dropout(const void* x, const void* residual, void* y, in
   P.nvec = (int)cdiv(N, 8);
   int sms = 148;
   if ((st = num_sms(&sms))) return st;
-  // two vectors a thread and trip; at most one resident wave of four 256-thread CTAs per SM
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(cdiv(M * (int64_t)P.nvec, 512), (int64_t)sms * 4));
-  const RowTypes types = row_types(P.vec && N % 8 == 0, x_dtype, y_dtype, x_dtype);
+  const RowTypes types = row_types(P.vec, M, N, x_dtype, y_dtype, x_dtype);
+  // at most one resident wave
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(cdiv(M * (int64_t)P.nvec, 256),
+                                                              (int64_t)sms * dropout_ctas(types != ROWS_ANY)));
   void (*fn)(DropoutArgs) = types == ROWS_BF16       ? fl_dropout_kernel<DT_BF16, DT_BF16>
                             : types == ROWS_F16      ? fl_dropout_kernel<DT_F16, DT_F16>
                             : types == ROWS_BF16_F32 ? fl_dropout_kernel<DT_BF16, DT_F32>
@@ -235,10 +238,10 @@ extern "C" fl_status fl_dropout_layernorm(const void* x, const void* residual, c
   P.N = (int)N;
   P.param_dt = param_dtype;
   P.eps = eps;
-  const RowKernel<DropLnArgs> k = ln_kernel(N, row_types(P.vec && N % 8 == 0, x_dtype, sum_dtype, z_dtype));
+  const RowKernel<DropLnArgs> k = ln_kernel(N, row_types(P.vec, M, N, x_dtype, sum_dtype, z_dtype));
   const int64_t ctas = cdiv(M, k.threads == 0 ? 1 : k.block / k.threads);
   size_t smem = 0;
-  if ((st = ring_of(k, operand_bytes(P.x, k.vecs, k.block) + operand_bytes(P.r, k.vecs, k.block), &P, &smem))) return st;
+  if ((st = ring_of(k, operand_bytes(P.x, k.vecs, k.block) + operand_bytes(P.r, k.vecs, k.block), 0, &P, &smem))) return st;
   int sms = 148, per_sm = 0;
   if ((st = num_sms(&sms))) return st;
   // one resident wave of CTAs that walk the rows: their rows ahead are then always in flight
@@ -291,7 +294,7 @@ extern "C" fl_status fl_dropout_layernorm_backward(
   int sms = 148;
   if ((st = num_sms(&sms))) return st;
   // (the geometry, and so the workspace, does not depend on the types)
-  const BwdGeom g = bwd_geom(M, N, sms, row_types(P.vec && N % 8 == 0, x_dtype, sum_dtype, z_dtype));
+  const BwdGeom g = bwd_geom(M, N, sms, row_types(P.vec, M, N, x_dtype, sum_dtype, z_dtype));
   const bool params = dgamma || dbeta;
   if (params && (!workspace || workspace_bytes < g.bytes || !aligned16(workspace)))
     return fail(FL_ERR_INVALID_ARG, "%s: dgamma and dbeta need a 16-byte aligned workspace of %zu bytes "
@@ -312,7 +315,8 @@ extern "C" fl_status fl_dropout_layernorm_backward(
   P.param_dt = param_dtype;
   size_t smem = 0;
   if ((st = ring_of(g.k, operand_bytes(P.dz, g.k.vecs, g.k.block) + operand_bytes(P.s, g.k.vecs, g.k.block) +
-                             operand_bytes(P.ds_in, g.k.vecs, g.k.block), &P, &smem)))
+                             operand_bytes(P.ds_in, g.k.vecs, g.k.block),
+                    g.k.threads == 0 || !P.ws ? 0 : ln_bwd_part_bytes(g.k.threads, g.k.vecs), &P, &smem)))
     return st;
   cudaError_t err = launch_pdl_smem(g.k.fn, dim3((unsigned)g.grid), (unsigned)g.k.block, smem, s, P);
   if (err != cudaSuccess) return fail(FL_ERR_CUDA, "%s: kernel launch: %s", who, cudaGetErrorString(err));

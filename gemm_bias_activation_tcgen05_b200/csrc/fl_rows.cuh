@@ -23,8 +23,9 @@ namespace fl {
 //
 // A round is two 32 x 32 -> 64 multiplications and two three-way exclusive ors: the round keys come
 // from the host, so that they are constant-bank operands, and what the first round makes of the
-// offset is the same for every element.  Ten rounds for four elements still are the largest part of
-// these kernels' instructions.
+// offset is the same for every element.  The multiplications (four cycles each of one of the SM's
+// pipes) are what bounds these kernels after the memory: that pipe was active for 73 % of the time
+// of an 8192 x 4096 bf16 dropout with residual (42 us).
 struct DropParams {
   uint32_t k0[10], k1[10];     // the rounds' keys, from the seed's halves
   uint64_t offset;             // upper counter half
@@ -34,22 +35,41 @@ struct DropParams {
   int on;                      // 0: p = 0, nothing is drawn
 };
 
-// What a thread keeps of the offset: the first round's share of the new words 0, 1 and 2.
+// What a thread keeps of the offset and the keys: everything that the first two rounds make of
+// them alone, for blocks below 2^32 (so that 18 multiplications remain of 20).
 struct DropOffset {
-  uint32_t w0, w1, w2;
+  uint32_t w0, w1, w2;      // round 1: shares of the new words 0, 1 and 2
+  uint32_t v0, v2, v3;      // round 2: shares of the new words 0, 2 and 3
 };
 __device__ __forceinline__ DropOffset drop_offset(const DropParams& d) {
   uint64_t off = d.offset;
   if (d.on && d.offset_dev != nullptr) off += *d.offset_dev;
   const uint64_t b = (uint64_t)(uint32_t)off * 0xCD9E8D57u;
-  return {(uint32_t)(b >> 32) ^ d.k0[0], (uint32_t)b, (uint32_t)(off >> 32) ^ d.k1[0]};
+  DropOffset o;
+  o.w0 = (uint32_t)(b >> 32) ^ d.k0[0];
+  o.w1 = (uint32_t)b;
+  o.w2 = (uint32_t)(off >> 32) ^ d.k1[0];
+  const uint64_t a = (uint64_t)o.w0 * 0xD2511F53u;
+  o.v0 = o.w1 ^ d.k0[1];
+  o.v2 = (uint32_t)(a >> 32) ^ d.k1[1];
+  o.v3 = (uint32_t)a;
+  return o;
 }
 
+// BIG: blocks may reach 2^32 (matrices of 2^34 elements and more, which run on the untyped kernels)
+template <bool BIG>
 __device__ __forceinline__ uint4 philox4x32_10(uint64_t block, const DropOffset& o, const DropParams& d) {
   const uint64_t first = (uint64_t)(uint32_t)block * 0xD2511F53u;
-  uint32_t c0 = o.w0 ^ (uint32_t)(block >> 32), c1 = o.w1, c2 = (uint32_t)(first >> 32) ^ o.w2, c3 = (uint32_t)first;
+  const uint32_t f2 = (uint32_t)(first >> 32) ^ o.w2, f3 = (uint32_t)first;
+  const uint64_t second = (uint64_t)f2 * 0xCD9E8D57u;
+  uint32_t c0 = (uint32_t)(second >> 32) ^ o.v0, c1 = (uint32_t)second, c2 = o.v2 ^ f3, c3 = o.v3;
+  if (BIG) {
+    const uint64_t a = (uint64_t)(o.w0 ^ (uint32_t)(block >> 32)) * 0xD2511F53u;
+    c2 = (uint32_t)(a >> 32) ^ f3 ^ d.k1[1];
+    c3 = (uint32_t)a;
+  }
 #pragma unroll
-  for (int r = 1; r < 10; ++r) {
+  for (int r = 2; r < 10; ++r) {
     const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
     c0 = (uint32_t)(b >> 32) ^ c1 ^ d.k0[r];
     c1 = (uint32_t)b;
@@ -59,28 +79,28 @@ __device__ __forceinline__ uint4 philox4x32_10(uint64_t block, const DropOffset&
   return make_uint4(c0, c1, c2, c3);
 }
 
-// r[i] + D(v)[i] for the eight elements of blocks `block` and `block` + 1.  A dropped element adds
-// nothing at all (not 0·v, which would keep a NaN); a kept one is one fused product and sum.
-__device__ __forceinline__ void add_dropped8(float (&r)[8], const float (&v)[8], uint64_t block, const DropOffset& o,
-                                             const DropParams& d) {
+// The random numbers of the eight elements of blocks `block` and `block` + 1.  Drawn while the
+// elements themselves are still on their way from memory.
+struct Draw8 {
+  uint4 a, b;
+};
+template <bool BIG>
+__device__ __forceinline__ Draw8 draw8(uint64_t block, const DropOffset& o, const DropParams& d) {
+  return {philox4x32_10<BIG>(block, o, d), philox4x32_10<BIG>(block + 1, o, d)};
+}
+// r[i] += D(v)[i].  A dropped element adds nothing at all (not 0·v, which would keep a NaN); a kept
+// one is one fused product and sum.
+__device__ __forceinline__ void add_dropped8(float (&r)[8], const float (&v)[8], const Draw8& w, const DropParams& d) {
+  const uint32_t x[8] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint4 w = philox4x32_10(block + h, o, d);
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (x[i] >= d.threshold) r[4 * h + i] = fmaf(v[4 * h + i], d.scale, r[4 * h + i]);
-  }
+  for (int i = 0; i < 8; ++i)
+    if (x[i] >= d.threshold) r[i] = fmaf(v[i], d.scale, r[i]);
 }
 // v = D(v)
-__device__ __forceinline__ void drop8(float (&v)[8], uint64_t block, const DropOffset& o, const DropParams& d) {
+__device__ __forceinline__ void drop8(float (&v)[8], const Draw8& w, const DropParams& d) {
+  const uint32_t x[8] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint4 w = philox4x32_10(block + h, o, d);
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[4 * h + i] = x[i] >= d.threshold ? v[4 * h + i] * d.scale : 0.0f;
-  }
+  for (int i = 0; i < 8; ++i) v[i] = x[i] >= d.threshold ? v[i] * d.scale : 0.0f;
 }
 
 // ---------------------------------------------------------------- eight elements of a row
@@ -126,8 +146,9 @@ __device__ __forceinline__ void widen8(float (&v)[8], const Raw8& r, int dt) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]), v[4 + i] = __uint_as_float(x[i]);
   } else if (dt == DT_BF16) {
+    // (a byte permutation, not a shift, which would go to the multiplications' pipe)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(__byte_perm(w[i], 0u, 0x1044)), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -223,9 +244,14 @@ struct DropoutArgs {
 
 // Thread i of the grid takes vectors i, i + threads, ... of the M·nvec (row, vector) pairs; row
 // and vector advance by the stride's quotient and remainder, so that one division runs per
-// thread.  Two vectors a trip: both vectors' loads are in flight before the first use.
+// thread.  The random numbers are drawn while the vectors are on their way.  One vector a trip and
+// all the warps an SM holds: 8192 x 4096 bf16 with a residual takes 37.4 us (5.4 TB/s; without the
+// drawing, p = 0, 30.4 us, the copy rate), two vectors and half the warps 42.4, and with two
+// vectors six CTAs 38.5.
+// (The untyped form needs more registers than eight CTAs leave it.)
+__host__ __device__ constexpr int dropout_ctas(bool typed) { return typed ? 8 : 4; }
 template <int XT, int YT>
-__global__ void __launch_bounds__(256, 4) fl_dropout_kernel(const DropoutArgs P) {
+__global__ void __launch_bounds__(256, dropout_ctas(XT >= 0)) fl_dropout_kernel(const DropoutArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   constexpr bool TYPED = XT >= 0;
@@ -240,45 +266,35 @@ __global__ void __launch_bounds__(256, 4) fl_dropout_kernel(const DropoutArgs P)
   const long long groups = (P.N + 3) / 4;
   const bool has_r = P.r.p != nullptr;
   while (row < P.M) {
-    long long rows[2];
-    int c0[2], cnt[2];
-    bool live[2], vec[2];
-    Raw8 rx[2], rr[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      rows[u] = row;
-      live[u] = row < P.M;
-      c0[u] = 8 * v;
-      cnt[u] = TYPED ? 8 : min(8, P.N - c0[u]);
-      vec[u] = TYPED || (P.vec && cnt[u] == 8);
-      if (live[u] && vec[u]) {
-        rx[u] = load_raw8(P.x, row, c0[u], xt);
-        if (has_r) rr[u] = load_raw8(P.r, row, c0[u], yt);
-      }
-      row += srow;
-      v += svec;
-      if (v >= P.nvec) v -= P.nvec, ++row;
+    const int c0 = 8 * v;
+    const int cnt = TYPED ? 8 : min(8, P.N - c0);
+    const bool vec = TYPED || (P.vec && cnt == 8);
+    Raw8 rx, rr;
+    if (vec) {
+      rx = load_raw8(P.x, row, c0, xt);
+      if (has_r) rr = load_raw8(P.r, row, c0, yt);
     }
+    Draw8 w;
+    if (P.d.on) w = draw8<!TYPED>((uint64_t)(row * groups + (c0 >> 2)), off, P.d);
+    float x[8], r[8];
+    if (vec) widen8(x, rx, xt);
+    else load_some8(x, P.x, row, c0, cnt);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (!live[u]) continue;
-      float x[8], r[8];
-      if (vec[u]) widen8(x, rx[u], xt);
-      else load_some8(x, P.x, rows[u], c0[u], cnt[u]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = 0.0f;
-      if (has_r) {
-        if (vec[u]) widen8(r, rr[u], yt);
-        else load_some8(r, P.r, rows[u], c0[u], cnt[u]);
-      }
-      if (P.d.on) {
-        add_dropped8(r, x, (uint64_t)(rows[u] * groups + (c0[u] >> 2)), off, P.d);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] += x[i];
-      }
-      store8(P.y, rows[u], c0[u], cnt[u], vec[u], r, yt);
+    for (int i = 0; i < 8; ++i) r[i] = 0.0f;
+    if (has_r) {
+      if (vec) widen8(r, rr, yt);
+      else load_some8(r, P.r, row, c0, cnt);
     }
+    if (P.d.on) {
+      add_dropped8(r, x, w, P.d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] += x[i];
+    }
+    store8(P.y, row, c0, cnt, vec, r, yt);
+    row += srow;
+    v += svec;
+    if (v >= P.nvec) v -= P.nvec, ++row;
   }
 }
 
@@ -324,6 +340,13 @@ __device__ __forceinline__ float row_sum(float v, float2* red2, int& flip, int g
     v = a.x + a.y;
   }
   return v;
+}
+
+// a/n for a row length n, with inv = 1/n: one step of Newton's iteration on the rounded product
+// (three instructions, against a dozen for a division)
+__device__ __forceinline__ float div_n(float a, float n, float inv) {
+  const float q = a * inv;
+  return fmaf(fmaf(-q, n, a), inv, q);
 }
 
 // ---------------------------------------------------------------- rows ahead in shared memory
@@ -380,7 +403,7 @@ struct DropLnArgs {
 // registers (but for 1024 threads, which have 64 each).
 __host__ __device__ constexpr int ln_block(int t) { return t < 128 ? 128 : t; }
 template <int T, int V, int XT, int ST, int ZT>
-__global__ void __launch_bounds__(ln_block(T), T <= 128 ? 6 : T == 256 ? 3 : 1) fl_dropout_ln_kernel(const DropLnArgs P) {
+__global__ void __launch_bounds__(ln_block(T), T <= 128 ? 4 : T == 256 ? 2 : 1) fl_dropout_ln_kernel(const DropLnArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   constexpr bool TYPED = XT >= 0, HOIST = T < 1024;
@@ -393,7 +416,7 @@ __global__ void __launch_bounds__(ln_block(T), T <= 128 ? 6 : T == 256 ? 3 : 1) 
   int flip = 0;
   const DropOffset off = drop_offset(P.d);
   const long long groups = (P.N + 3) / 4;
-  const float n_f = (float)P.N;
+  const float n_f = (float)P.N, inv_n = 1.0f / n_f;
   const long long m0 = (long long)blockIdx.x * R + group, step = (long long)gridDim.x * R;
   const uint32_t ring = smem_u32(ring_s);
   const uint32_t xb = operand_bytes(P.x, V, BLOCK), slot_bytes = xb + operand_bytes(P.r, V, BLOCK);
@@ -434,6 +457,11 @@ __global__ void __launch_bounds__(ln_block(T), T <= 128 ? 6 : T == 256 ? 3 : 1) 
     const uint32_t slot = ring + at * slot_bytes;
     float s[V][8];
     float2 sum2 = make_float2(0.0f, 0.0f);
+    Draw8 w[V];
+    if (P.d.on) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) w[k] = draw8<!TYPED>((uint64_t)(m * groups + 2 * (k * T + t)), off, P.d);
+    }
     wait_row(P.ahead);  // this row's copies have landed
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -450,7 +478,7 @@ __global__ void __launch_bounds__(ln_block(T), T <= 128 ? 6 : T == 256 ? 3 : 1) 
         else load_some8(s[k], P.r, m, c0, cnt);
       }
       if (P.d.on) {
-        add_dropped8(s[k], x, (uint64_t)(m * groups + (c0 >> 2)), off, P.d);
+        add_dropped8(s[k], x, w[k], P.d);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) put_pair(s[k], j, add2(pair_of(s[k], j), pair_of(x, j)));
@@ -462,7 +490,7 @@ __global__ void __launch_bounds__(ln_block(T), T <= 128 ? 6 : T == 256 ? 3 : 1) 
     }
     prefetch(m + P.ahead * step, slot);  // (the slot's values are in registers)
     at = at + 1 == P.ahead ? 0 : at + 1;
-    const float mean = row_sum<T>(sum2.x + sum2.y, red_s[group], flip, group) / n_f;
+    const float mean = div_n(row_sum<T>(sum2.x + sum2.y, red_s[group], flip, group), n_f, inv_n);
     float2 q2 = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -476,7 +504,7 @@ __global__ void __launch_bounds__(ln_block(T), T <= 128 ? 6 : T == 256 ? 3 : 1) 
         q2 = fma2(d, d, q2);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<T>(q2.x + q2.y, red_s[group], flip, group) / n_f + P.eps);
+    const float rstd = 1.0f / sqrtf(div_n(row_sum<T>(q2.x + q2.y, red_s[group], flip, group), n_f, inv_n) + P.eps);
     if (t == 0 && P.mean != nullptr) P.mean[m] = mean, P.rstd[m] = rstd;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -506,7 +534,7 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_long_kernel(const DropLnAr
   int flip = 0;
   const DropOffset off = drop_offset(P.d);
   const long long groups = (P.N + 3) / 4;
-  const float n_f = (float)P.N;
+  const float n_f = (float)P.N, inv_n = 1.0f / n_f;
   for (long long m = blockIdx.x; m < P.M; m += gridDim.x) {
     auto value = [&](int c0, int cnt, bool vec, float (&s)[8]) {
       float x[8];
@@ -519,7 +547,7 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_long_kernel(const DropLnAr
         else load_some8(s, P.r, m, c0, cnt);
       }
       if (P.d.on) {
-        add_dropped8(s, x, (uint64_t)(m * groups + (c0 >> 2)), off, P.d);
+        add_dropped8(s, x, draw8<true>((uint64_t)(m * groups + (c0 >> 2)), off, P.d), P.d);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] += x[i];
@@ -550,8 +578,8 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_long_kernel(const DropLnAr
           store8(P.z, m, c0, cnt, vec, g, P.z.dt);
         }
       }
-      if (step == 0) mean = row_sum<1024>(acc, red, flip, 0) / n_f;
-      if (step == 1) rstd = 1.0f / sqrtf(row_sum<1024>(acc, red, flip, 0) / n_f + P.eps);
+      if (step == 0) mean = div_n(row_sum<1024>(acc, red, flip, 0), n_f, inv_n);
+      if (step == 1) rstd = 1.0f / sqrtf(div_n(row_sum<1024>(acc, red, flip, 0), n_f, inv_n) + P.eps);
     }
     if (threadIdx.x == 0 && P.mean != nullptr) P.mean[m] = mean, P.rstd[m] = rstd;
   }
@@ -569,15 +597,19 @@ struct DropLnBwdArgs {
 };
 
 // With u = (s − μ)·rstd and g = dz·γ:  ds = rstd·(g − mean(g) − u·mean(g·u)) + ds_in,
-// dx = D(ds), dγ = Σ_m dz·u, dβ = Σ_m dz.  T threads share a row, V vectors each, staged rows
-// ahead in shared memory (V > 1: read from there twice, for the sums and for the gradients), so that
-// registers hold little beside the dγ, dβ sums of the thread's columns, which it keeps over all its
-// rows.  A CTA of 512 (or T) threads holds R rows at a time; at the end its row groups add their
-// sums in turn in shared memory and store one partial row each of dγ and dβ, which
+// dx = D(ds), dγ = Σ_m dz·u, dβ = Σ_m dz.  T threads share a row, two vectors each, staged rows
+// ahead in shared memory; registers hold the row's g and u, γ, and the dγ, dβ sums of the thread's
+// columns over all its rows (1024 threads, which have half the registers, read the row from shared
+// memory twice instead, for the sums and for the gradients).  A CTA of 256 (or T) threads holds R rows at a time; at the end its row groups' sums are
+// added in shared memory and stored as one partial row each of dγ and dβ, which
 // fl_ln_wgrad_kernel adds in a fixed order.
-__host__ __device__ constexpr int ln_bwd_block(int t) { return t < 512 ? 512 : t; }
+__host__ __device__ constexpr int ln_bwd_block(int t) { return t < 256 ? 256 : t; }
+// bytes of the row groups' column sums at the end
+__host__ __device__ constexpr size_t ln_bwd_part_bytes(int t, int v) {
+  return ln_bwd_block(t) > t ? (size_t)(ln_bwd_block(t) / t) * 16u * (size_t)v * (size_t)t * sizeof(float) : 0;
+}
 template <int T, int V, int XT, int ST, int ZT>
-__global__ void __launch_bounds__(ln_bwd_block(T), T < 1024 ? 2 : 1) fl_dropout_ln_bwd_kernel(const DropLnBwdArgs P) {
+__global__ void __launch_bounds__(ln_bwd_block(T), T <= 256 ? 2 : 1) fl_dropout_ln_bwd_kernel(const DropLnBwdArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   constexpr bool TYPED = XT >= 0;
@@ -585,13 +617,12 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T < 1024 ? 2 : 1) fl_dropout_
   constexpr int R = BLOCK / T;
   extern __shared__ __align__(16) uint8_t ring_s[];
   __shared__ __align__(16) float2 red_s[R][2 * (T / 32)];
-  __shared__ float part_s[R > 1 ? 16 * V * T : 1];
   const int xt = dt_of<XT>(P.dx), st = dt_of<ST>(P.s), zt = dt_of<ZT>(P.dz);
   const int group = threadIdx.x / T, t = threadIdx.x % T;
   int flip = 0;
   const DropOffset off = drop_offset(P.d);
   const long long groups = (P.N + 3) / 4;
-  const float n_f = (float)P.N;
+  const float n_f = (float)P.N, inv_n = 1.0f / n_f;
   const long long m0 = (long long)blockIdx.x * R + group, step = (long long)gridDim.x * R;
   const uint32_t ring = smem_u32(ring_s);
   const uint32_t zb = operand_bytes(P.dz, V, BLOCK), sb = operand_bytes(P.s, V, BLOCK);
@@ -625,8 +656,14 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T < 1024 ? 2 : 1) fl_dropout_
     const int cnt = count(k);
     load_param8(g, P.gamma, P.param_dt, 8 * (k * T + t), cnt, TYPED || (P.vec && cnt == 8), 1.0f);
   };
-  float gam[8];
-  if (V == 1 && count(0) > 0) param(0, gam);
+  constexpr bool KEEP = T < 1024 || V == 1;  // the row's values and γ stay in registers
+  constexpr int VK = KEEP ? V : 1;
+  float gam[VK][8];
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (count(k) > 0) param(k, gam[k]);
+  }
   int at = 0;
   for (long long m = m0; m < P.M; m += step) {
     const uint32_t slot = ring + at * slot_bytes;
@@ -649,37 +686,39 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T < 1024 ? 2 : 1) fl_dropout_
     };
     wait_row(P.ahead);
     float2 a2 = make_float2(0.0f, 0.0f), b2 = a2;
-    float g[8], u[8];
+    float g[VK][8], u[VK][8];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int cnt = count(k);
       if (cnt == 0) continue;
-      values(k, cnt, g, u);
-      if constexpr (V > 1) param(k, gam);
+      const int kk = KEEP ? k : 0;
+      values(k, cnt, g[kk], u[kk]);
+      if constexpr (!KEEP) param(k, gam[kk]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 z = pair_of(g, j), w = pair_of(u, j);
+        const float2 z = pair_of(g[kk], j), w = pair_of(u[kk], j);
         put_pair(pg[k], j, fma2(z, w, pair_of(pg[k], j)));
         put_pair(pb[k], j, add2(z, pair_of(pb[k], j)));
         // (past the row dz is 0; a γ read there is not: only dz·γ enters the sums)
-        float2 q = mul2(z, pair_of(gam, j));
-        put_pair(g, j, q);
+        float2 q = mul2(z, pair_of(gam[kk], j));
+        put_pair(g[kk], j, q);
         a2 = add2(a2, q);
         b2 = fma2(q, w, b2);
       }
     }
     const float2 ab = row_sum2<T>(make_float2(a2.x + a2.y, b2.x + b2.y), red_s[group], flip, group);
-    const float ma = ab.x / n_f, mb = ab.y / n_f;
+    const float ma = div_n(ab.x, n_f, inv_n), mb = div_n(ab.y, n_f, inv_n);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int c0 = 8 * (k * T + t), cnt = count(k);
       if (cnt == 0) continue;
       const bool vec = TYPED || (P.vec && cnt == 8);
-      if constexpr (V > 1) {
-        values(k, cnt, g, u);
-        param(k, gam);
+      const int kk = KEEP ? k : 0;
+      if constexpr (!KEEP) {
+        values(k, cnt, g[0], u[0]);
+        param(k, gam[0]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) put_pair(g, j, mul2(pair_of(g, j), pair_of(gam, j)));
+        for (int j = 0; j < 4; ++j) put_pair(g[0], j, mul2(pair_of(g[0], j), pair_of(gam[0], j)));
       }
       float in[8];
 #pragma unroll
@@ -690,12 +729,12 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T < 1024 ? 2 : 1) fl_dropout_
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 q = fma2(pair_of(u, j), make_float2(-mb, -mb), add2(pair_of(g, j), make_float2(-ma, -ma)));
+        const float2 q = fma2(pair_of(u[kk], j), make_float2(-mb, -mb), add2(pair_of(g[kk], j), make_float2(-ma, -ma)));
         put_pair(in, j, fma2(q, make_float2(rstd, rstd), pair_of(in, j)));
       }
       if (P.dres.p != nullptr) store8(P.dres, m, c0, cnt, vec, in, st);
       if (P.dx.p != nullptr) {
-        if (P.d.on) drop8(in, (uint64_t)(m * groups + (c0 >> 2)), off, P.d);
+        if (P.d.on) drop8(in, draw8<!TYPED>((uint64_t)(m * groups + (c0 >> 2)), off, P.d), P.d);
         store8(P.dx, m, c0, cnt, vec, in, xt);
       }
     }
@@ -706,23 +745,31 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T < 1024 ? 2 : 1) fl_dropout_
   if (P.ws == nullptr) return;
   float* out = P.ws + (long long)blockIdx.x * 2 * P.ws_ld;
   if constexpr (R > 1) {
+    // every group's sums side by side in the ring's memory, then each thread adds the R sums of its
+    // share of the columns in group order
     constexpr int W = 8 * V * T;
-    for (int gr = 0; gr < R; ++gr) {
-      if (group == gr) {
+    float* part_s = reinterpret_cast<float*>(ring_s);
+    __syncthreads();  // the ring is free
 #pragma unroll
-        for (int k = 0; k < V; ++k)
+    for (int k = 0; k < V; ++k)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int c = (i * V + k) * T + t;  // (a warp's lanes side by side: no bank conflicts)
-            if (gr > 0) pg[k][i] += part_s[c], pb[k][i] += part_s[W + c];
-            part_s[c] = pg[k][i];
-            part_s[W + c] = pb[k][i];
-          }
+      for (int i = 0; i < 8; ++i) {
+        const int c = (i * V + k) * T + t;  // (a warp's lanes side by side: no bank conflicts)
+        part_s[group * 2 * W + c] = pg[k][i];
+        part_s[group * 2 * W + W + c] = pb[k][i];
       }
-      __syncthreads();
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2 * W / BLOCK; ++q) {
+      const int e = q * BLOCK + (int)threadIdx.x;
+      float v = part_s[e];
+#pragma unroll
+      for (int gr = 1; gr < R; ++gr) v += part_s[gr * 2 * W + e];
+      const int j = e % W;
+      const int c = 8 * (j / T % V * T + j % T) + j / (V * T);
+      if (c < P.N) out[e / W * P.ws_ld + c] = v;
     }
-  }
-  if (group == R - 1) {  // (the last group's registers hold the sums of all)
+  } else {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int c0 = 8 * (k * T + t);
@@ -747,7 +794,7 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_bwd_long_kernel(const Drop
   int flip = 0;
   const DropOffset off = drop_offset(P.d);
   const long long groups = (P.N + 3) / 4;
-  const float n_f = (float)P.N;
+  const float n_f = (float)P.N, inv_n = 1.0f / n_f;
   float* out = P.ws == nullptr ? nullptr : P.ws + (long long)blockIdx.x * 2 * P.ws_ld;
   for (long long m = blockIdx.x; m < P.M; m += gridDim.x) {
     const float mean = P.mean[m], rstd = P.rstd[m];
@@ -795,15 +842,15 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_bwd_long_kernel(const Drop
           }
           if (P.dres.p != nullptr) store8(P.dres, m, c0, cnt, vec, dz, P.dres.dt);
           if (P.dx.p != nullptr) {
-            if (P.d.on) drop8(dz, (uint64_t)(m * groups + (c0 >> 2)), off, P.d);
+            if (P.d.on) drop8(dz, draw8<true>((uint64_t)(m * groups + (c0 >> 2)), off, P.d), P.d);
             store8(P.dx, m, c0, cnt, vec, dz, P.dx.dt);
           }
         }
       }
       if (step == 0) {
         const float2 ab = row_sum2<1024>(make_float2(a, b), red, flip, 0);
-        ma = ab.x / n_f;
-        mb = ab.y / n_f;
+        ma = div_n(ab.x, n_f, inv_n);
+        mb = div_n(ab.y, n_f, inv_n);
       }
     }
   }

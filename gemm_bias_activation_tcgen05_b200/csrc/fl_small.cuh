@@ -1,0 +1,148 @@
+// fl_small.cuh — the gated linear unit of a few rows (serving: one new token of each of up to 32
+// sequences): h = act(x·Wgᵀ) ⊙ (x·Wuᵀ), bound by reading the weights once.
+//
+// A warp owns 8 output features: their 8 gate rows and 8 up rows of W are the 16 rows of an
+// mma.sync.m16n8k16 operand A, the rows of x its B columns (8 at a time), so that gate and up of a
+// feature end in the same lane.  An inner product does not depend on the order of k, so the lanes
+// take k in an order of their own: in a step of 32 lane (g, t) holds k = 8t .. 8t + 7 of row g, one
+// 16-byte load, whose four words are the k pairs of two products, and the same k of x's row g.
+// Weights go from memory to the tensor core through registers: no shared memory, no barrier.
+// The products run far below the tensor core's rate (2·M operations a byte), so the legacy warp form
+// is enough, and it needs no staging.  The CTA's warps share the 8 features and take steps of k in
+// turn, four steps (256 bytes of each of 16 rows) at a time, all in flight; their sums meet in shared
+// memory in a fixed order.
+#pragma once
+#include "fl_pair.cuh"
+
+namespace fl {
+
+constexpr int kSmallWarps = 8;
+constexpr int kSmallUnroll = 4;   // steps of 32 k in flight
+constexpr int kSmallMaxRows = 32;
+
+struct SmallArgs {
+  const void *x, *w;
+  void* out;
+  int M, N, K;
+  long long ldx, ldw, ldo;
+  int out_dt;
+};
+
+// 16 bytes that are read once
+__device__ __forceinline__ uint4 ldg_stream(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+// elements k .. k + 7 of a row of K, zeros past its end
+__device__ __forceinline__ uint4 ldg_tail(const uint16_t* row, int k, int K) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = k + 2 * i < K ? row[k + 2 * i] : 0u, hi = k + 2 * i + 1 < K ? row[k + 2 * i + 1] : 0u;
+    w[i] = lo | (hi << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// d += A·B: A rows 0..7 (a0, a2) and 8..15 (a1, a3), B (b0, b1)
+template <int DT>
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  if constexpr (DT == DT_BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: blocks of 8 rows of x (M ≤ 8·NT)
+template <int ACT, int DT, int NT>
+__global__ void __launch_bounds__(kSmallWarps * 32, NT <= 2 ? 3 : 2) fl_glu_small_kernel(const SmallArgs P) {
+  constexpr int U = kSmallUnroll, W = kSmallWarps;
+  __shared__ float part[W][2][8][8 * NT + 1];  // [warp][gate, up][feature][row of x]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * 8;
+  const bool n_ok = n0 + g < P.N;
+  const uint16_t* wg = reinterpret_cast<const uint16_t*>(P.w) + (long long)(n0 + g) * P.ldw;
+  const uint16_t* wu = wg + (long long)P.N * P.ldw;
+  const uint16_t* xr = reinterpret_cast<const uint16_t*>(P.x) + (long long)g * P.ldx;
+  float acc[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
+
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const int whole = P.K / (32 * U);  // groups of U whole steps
+  for (int s = warp; s < whole; s += W) {
+    const int k0 = s * 32 * U + 8 * t;
+    uint4 a[U], b[U], x[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      a[u] = n_ok ? ldg_stream(wg + k0 + 32 * u) : zero;
+      b[u] = n_ok ? ldg_stream(wu + k0 + 32 * u) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        x[u][j] = g + 8 * j < P.M ? *reinterpret_cast<const uint4*>(xr + (long long)(8 * j) * P.ldx + k0 + 32 * u) : zero;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        mma_16816<DT>(acc[j], a[u].x, b[u].x, a[u].y, b[u].y, x[u][j].x, x[u][j].y);
+        mma_16816<DT>(acc[j], a[u].z, b[u].z, a[u].w, b[u].w, x[u][j].z, x[u][j].w);
+      }
+  }
+  // the last steps, one at a time
+  for (int s = whole * U + warp; 32 * s < P.K; s += W) {
+    const int k = 32 * s + 8 * t;
+    const bool in = k + 8 <= P.K, some = k < P.K;
+    uint4 a = zero, b = zero;
+    if (n_ok && some) {
+      a = in ? ldg_stream(wg + k) : ldg_tail(wg, k, P.K);
+      b = in ? ldg_stream(wu + k) : ldg_tail(wu, k, P.K);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      uint4 x = zero;
+      if (g + 8 * j < P.M && some) {
+        const uint16_t* r = xr + (long long)(8 * j) * P.ldx;
+        x = in ? *reinterpret_cast<const uint4*>(r + k) : ldg_tail(r, k, P.K);
+      }
+      mma_16816<DT>(acc[j], a.x, b.x, a.y, b.y, x.x, x.y);
+      mma_16816<DT>(acc[j], a.z, b.z, a.w, b.w, x.z, x.w);
+    }
+  }
+  // lane (g, t): gate and up of feature g and x's rows 8j + 2t, 8j + 2t + 1
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    part[warp][0][g][8 * j + 2 * t] = acc[j][0];
+    part[warp][0][g][8 * j + 2 * t + 1] = acc[j][1];
+    part[warp][1][g][8 * j + 2 * t] = acc[j][2];
+    part[warp][1][g][8 * j + 2 * t + 1] = acc[j][3];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 8 * P.M; e += W * 32) {
+    const int f = e & 7, m = e >> 3;
+    float vg = 0.0f, vu = 0.0f, slope;
+#pragma unroll
+    for (int w = 0; w < W; ++w) vg += part[w][0][f][m], vu += part[w][1][f][m];
+    const float h = gate_f<ACT>(vg, slope) * vu;
+    if (n0 + f < P.N) {
+      const long long o = (long long)m * P.ldo + n0 + f;
+      if (P.out_dt == DT_BF16) store_elem<DT_BF16>(P.out, o, h);
+      else store_elem<DT_F16>(P.out, o, h);
+    }
+  }
+}
+
+}  // namespace fl
