@@ -30,8 +30,13 @@ template <int EPI, int ACT>
 PairFn by_out(int out) {
   return out == FL_BF16 ? &fl_pair_tcgen05<EPI, ACT, DT_BF16> : &fl_pair_tcgen05<EPI, ACT, DT_F16>;
 }
-// `out`: the type that the kernel itself writes (fp32 partial tiles with K splits)
-PairFn pair_kernel(int kind, int out) {
+PairFn pair_kernel(int kind, int out, bool split) {
+  const int epi = epi_of(kind);
+  if (split) {
+    return epi == EPI_GRAD   ? &fl_pair_tcgen05<EPI_GRAD, GATE_SWIGLU, DT_F32>
+           : epi == EPI_DGLU ? &fl_pair_tcgen05<EPI_DGLU_PART, GATE_SWIGLU, DT_F32>
+                             : &fl_pair_tcgen05<EPI_GLU_PART, GATE_SWIGLU, DT_F32>;
+  }
   switch (kind) {
     case FL_EPI_SWIGLU: return by_out<EPI_GLU, GATE_SWIGLU>(out);
     case FL_EPI_GEGLU_TANH_AUX: return by_out<EPI_GLU_AUX, GATE_GEGLU_TANH>(out);
@@ -41,12 +46,41 @@ PairFn pair_kernel(int kind, int out) {
     default: return out == FL_F32 ? &fl_pair_tcgen05<EPI_GRAD, GATE_SWIGLU, DT_F32> : by_out<EPI_GRAD, GATE_SWIGLU>(out);
   }
 }
+void (*finish_kernel(int kind))(FinishArgs) {
+  switch (epi_of(kind)) {
+    case EPI_GRAD: return fl_split_finish_kernel<EPI_GRAD, GATE_SWIGLU>;
+    case EPI_DGLU:
+      return is_geglu(kind) ? fl_split_finish_kernel<EPI_DGLU, GATE_GEGLU_TANH> : fl_split_finish_kernel<EPI_DGLU, GATE_SWIGLU>;
+    default:
+      return is_geglu(kind) ? fl_split_finish_kernel<EPI_GLU, GATE_GEGLU_TANH> : fl_split_finish_kernel<EPI_GLU, GATE_SWIGLU>;
+  }
+}
+// What the tile kernel itself computes and writes: with K splits, fp32 partial results.
+int kernel_epi(const fl_plan_s* p) {
+  const int epi = epi_of(p->epi.kind);
+  if (p->split_k == 1 || epi == EPI_GRAD) return epi;
+  return epi == EPI_DGLU ? EPI_DGLU_PART : EPI_GLU_PART;
+}
 int kernel_out(const fl_plan_s* p) { return p->split_k > 1 ? FL_F32 : p->epi.out_dtype; }
 
-// Rows and pitch of one split's partial tiles in the workspace: whole 256-row tiles, and rows of
-// whole 32-column blocks.
-int64_t split_rows(const fl_plan_s* p) { return 256LL * p->tiles_a; }
-int64_t ws_ld(const fl_plan_s* p) { return cdiv(p->N, 32) * 32; }
+// Shared memory of the tile kernel: the ring, the epilogue warps' blocks, the barriers.
+struct PairLayout {
+  uint32_t stage, staging, bar_off, total;
+};
+PairLayout pair_layout(const fl_plan_s* p) {
+  PairLayout L;
+  L.stage = kPairABytes + (uint32_t)(p->mma_n / 2) * 128u;
+  L.staging = 8u * pair_warp_staging(kernel_epi(p), kernel_out(p));
+  L.bar_off = (uint32_t)p->stages * L.stage + L.staging;
+  L.total = L.bar_off + kPairBarBytes + 1024u;  // (the ring starts on the next 1024 bytes)
+  return L;
+}
+
+// The workspace of a result in K splits: rows of one split (whole 32-row blocks), columns of one
+// partial result (whole 32-column blocks) and of a row (GLU: g and u side by side).
+int64_t split_rows(const fl_plan_s* p) { return cdiv(p->M, 32) * 32; }
+int64_t part_cols(const fl_plan_s* p) { return cdiv(p->N, 32) * 32; }
+int64_t ws_ld(const fl_plan_s* p) { return part_cols(p) * (pair_glu(epi_of(p->epi.kind)) ? 2 : 1); }
 
 }  // namespace
 
@@ -69,14 +103,13 @@ fl_status fl::host::pair_check(const char* who, int64_t M, int64_t N, int64_t K,
   return FL_OK;
 }
 
-// Tile width, K splits, stages and grid.
+// Tile width, K splits, stages and grid, by an estimate of the time of each choice.
 //  * A tile is 256 rows by 256 accumulator columns (GLU: 128 gate and 128 up), or by 128 where
-//    narrower tiles take fewer or better filled rounds of the GPU's pairs.
-//  * GRAD: a gradient of few tiles would leave most pairs idle while each walks all tokens, so K is
-//    cut into S splits; S minimises the estimated time below.
+//    narrower tiles fill the GPU's pairs better.
+//  * Where few tiles would leave most pairs idle while each walks all of K, K is cut into S splits.
 fl_status fl::host::pair_config(fl_plan_s* p, bool no_workspace) {
   const int epi = epi_of(p->epi.kind);
-  const bool glu = epi == EPI_GLU || epi == EPI_GLU_AUX;
+  const bool glu = pair_glu(epi);
   const int64_t P = std::max(1, p->num_sms / 2);
   p->swap = false;
   p->small = false;
@@ -87,17 +120,22 @@ fl_status fl::host::pair_config(fl_plan_s* p, bool no_workspace) {
   p->pair = true;
   p->k_atoms = 1;
   p->num_kb = (int)cdiv(p->K, kPairBk);
+  const double M = (double)p->M, N = (double)p->N, K = (double)p->K, cols = glu ? 2 * N : N;
   double best = 1e300;
   for (int width : {256, 128}) {
     const int64_t tiles = cdiv(p->M, 256) * cdiv(p->N, glu ? width / 2 : width);
-    // microseconds of a 64-deep K block, and of what a tile adds outside its K loop
-    const double block_us = width == 256 ? 0.29 : 0.19, tile_us = width == 256 ? 2.0 : 1.5;
-    const int most = epi == EPI_GRAD && !no_workspace ? std::min(p->num_kb, 32) : 1;
+    // microseconds of a 64-deep K block, and of what a unit adds outside its K loop
+    const double block_us = width == 256 ? 0.40 : 0.30, unit_us = 2.5;
+    const int most = no_workspace ? 1 : std::min(p->num_kb, 32);
     for (int S = 1; S <= std::max(1, most); ++S) {
-      if (tiles * S >= (1LL << 24)) break;  // the tile raster's range
-      double us = (double)cdiv(tiles * S, P) * ((double)cdiv(p->num_kb, S) * block_us + tile_us);
-      // the partial tiles are written and read once more (mostly through L2), by one more launch
-      if (S > 1) us += 3.0 + (double)S * 8.0 * (double)p->M * (double)p->N / 8e6;
+      const int64_t units = tiles * S;
+      if (units >= (1LL << 24) || (S > 1 && units > 2 * P)) break;  // (the tile raster's range; the workspace's size)
+      double us = (double)cdiv(units, P) * ((double)cdiv(p->num_kb, S) * block_us + unit_us);
+      // every operand comes from memory once, by the SMs that are busy
+      const double bytes = 2.0 * (M * K + cols * K + (epi == EPI_GRAD ? 2.0 : 3.0) * M * N);
+      us = std::max(us, bytes / (6.0e6 * std::min(1.0, (double)units / (double)P)));
+      // the partial results are written and read once more (mostly in L2), by one more launch
+      if (S > 1) us += 3.5 + (double)S * 8.0 * M * cols / 8e6;
       if (us < best) {
         best = us;
         p->mma_n = width;
@@ -109,14 +147,13 @@ fl_status fl::host::pair_config(fl_plan_s* p, bool no_workspace) {
   p->out_tile_n = glu ? p->mma_n / 2 : p->mma_n;
   p->tiles_a = (int)cdiv(p->M, 256);
   p->tiles_b = (int)cdiv(p->N, p->out_tile_n);
-  const uint32_t staging = 8u * pair_warp_staging(epi, kernel_out(p));
-  const uint32_t stage = kPairABytes + (uint32_t)(p->mma_n / 2) * 128u;
-  const int64_t room = (int64_t)p->max_smem - 1024 - staging - kPairBarBytes;
-  p->stages = (int)std::min<int64_t>(12, std::max<int64_t>(0, room) / stage);
+  p->stages = 0;
+  const PairLayout none = pair_layout(p);
+  p->stages = (int)std::min<int64_t>(12, std::max<int64_t>(0, (int64_t)p->max_smem - none.total) / none.stage);
   if (p->stages < 2) return fail(FL_ERR_UNSUPPORTED, "fl_plan: shared memory too small");
-  p->smem = (int)(1024 + (uint32_t)p->stages * stage + staging + kPairBarBytes);
+  p->smem = (int)pair_layout(p).total;
   p->grid = (int)(2 * std::min<int64_t>((int64_t)p->tiles_a * p->tiles_b * p->split_k, P));
-  p->kernel = reinterpret_cast<const void*>(pair_kernel(p->epi.kind, kernel_out(p)));
+  p->kernel = reinterpret_cast<const void*>(pair_kernel(p->epi.kind, p->epi.out_dtype, p->split_k > 1));
   p->launches = p->split_k > 1 ? 2 : 1;
   return FL_OK;
 }
@@ -135,15 +172,15 @@ fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, voi
                                  cudaStream_t stream) {
   if (p->small) return small_execute(p, A, W, out, stream);
   const fl_epilogue_desc& e = p->epi;
-  const int epi = epi_of(e.kind);
+  const int epi = kernel_epi(p);
   const bool split = p->split_k > 1;
-  const int kout = kernel_out(p);
+  const PairLayout L = pair_layout(p);
   const uint64_t es = 2, eo = (uint64_t)esize(e.out_dtype);
   const uint64_t M = (uint64_t)p->M, N = (uint64_t)p->N, K = (uint64_t)p->K;
 
   KParams k{};
   k.M = (int)p->M;
-  k.N = split ? (int)ws_ld(p) : (int)p->N;
+  k.N = split ? (int)part_cols(p) : (int)p->N;
   k.K = (int)p->K;
   k.tiles_a = p->tiles_a;
   k.tiles_b = p->tiles_b;
@@ -153,13 +190,13 @@ fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, voi
   k.mma_n = p->mma_n;
   k.out_tile_n = p->out_tile_n;
   k.b_boxes = p->mma_n / 128;  // 64-column boxes of this CTA's half of an MN-major B
-  k.stage_bytes = k.stage_stride = kPairABytes + (uint32_t)(p->mma_n / 2) * 128u;
+  k.stage_bytes = k.stage_stride = L.stage;
   const uint32_t fmt = p->dtype == FL_BF16 ? 1u : 0u;
   k.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(pair_a_mn(epi) ? 1 : 0) << 15) |
             ((uint32_t)(pair_b_mn(epi) ? 1 : 0) << 16) | ((uint32_t)(p->mma_n >> 3) << 17) | ((256u >> 4) << 24);
   k.tmem_cols = (uint32_t)(2 * p->mma_n);
-  k.staging_off = (uint32_t)p->stages * k.stage_stride;
-  k.bar_off = k.staging_off + 8u * pair_warp_staging(epi, kout);
+  k.staging_off = L.bar_off - L.staging;
+  k.bar_off = L.bar_off;
   k.residual = split ? nullptr : residual;
   k.ldr = e.ldr;
   k.res_dtype = e.residual_dtype;
@@ -205,7 +242,7 @@ fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, voi
     k.n_tma = (int)N;
   } else if (split) {
     k.n_tma = k.N;
-    st = tile(&m0, p->d_skws, FL_F32, (uint64_t)k.N, (uint64_t)p->split_k * (uint64_t)split_rows(p), (uint64_t)k.N * 4);
+    st = tile(&m0, p->d_skws, FL_F32, (uint64_t)ws_ld(p), (uint64_t)p->split_k * (uint64_t)split_rows(p), (uint64_t)ws_ld(p) * 4);
     if (st) return st;
   } else {
     // whole 16-byte granules of a row go out by TMA, the ragged remainder by plain stores
@@ -237,10 +274,11 @@ fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, voi
   if ((st = after_launch(stream, "pair kernel"))) return st;
   if (!split) return FL_OK;
 
-  GradReduceArgs r{};
+  FinishArgs r{};
   r.ws = p->d_skws;
   r.split_stride = split_rows(p) * ws_ld(p);
   r.ld_ws = ws_ld(p);
+  r.half = part_cols(p);
   r.splits = p->split_k;
   r.residual = residual;
   r.ldr = e.ldr;
@@ -248,13 +286,14 @@ fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, voi
   r.out = out;
   r.ldo = e.ldo;
   r.out_dtype = e.out_dtype;
+  r.aux = aux;
   r.M = p->M;
   r.N = (int)p->N;
   r.nvec = (int)cdiv(p->N, 4);
   r.scale = e.scale;
   const int64_t work = p->M * (int64_t)r.nvec;
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(cdiv(work, 256), (int64_t)p->num_sms * 8));
-  err = launch_pdl_b(fl_grad_reduce_kernel, dim3(grid), 256u, stream, r);
-  if (err != cudaSuccess) return fail(FL_ERR_CUDA, "reduction kernel launch: %s", cudaGetErrorString(err));
-  return after_launch(stream, "weight gradient reduction");
+  err = launch_pdl_b(finish_kernel(e.kind), dim3(grid), 256u, stream, r);
+  if (err != cudaSuccess) return fail(FL_ERR_CUDA, "finishing kernel launch: %s", cudaGetErrorString(err));
+  return after_launch(stream, "epilogue after K splits");
 }

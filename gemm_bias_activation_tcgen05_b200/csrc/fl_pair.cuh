@@ -8,9 +8,11 @@
 //                stored g, u: dh never leaves the chip
 //   EPI_GRAD     y = (Aᵀ·W + residual)·scale, A stored [K, M] and W stored [K, N]: the weight
 //                gradient, K the tokens.  Both operands are read as they lie, through MN-major UMMA
-//                descriptors, so nothing is transposed in memory.  When the tiles leave pairs idle, K
-//                is cut into splits whose fp32 partial tiles go to a workspace, which
-//                fl_grad_reduce_kernel adds in split order.
+//                descriptors, so nothing is transposed in memory.
+//
+// When the tiles would leave most pairs idle, K is cut into splits: the kernel then writes fp32
+// partial tiles to a workspace (EPI_GLU_PART, EPI_DGLU_PART; EPI_GRAD itself), and a second, small
+// kernel adds them in split order and does the epilogue.
 //
 // Roles (320 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM allocator and (rank 0 of
 // the pair) UMMA issuer, warps 2..9 epilogue, two per TMEM lane quarter, each with half of the
@@ -24,7 +26,7 @@
 
 namespace fl {
 
-enum PairEpi : int { EPI_GLU = 0, EPI_GLU_AUX = 1, EPI_DGLU = 2, EPI_GRAD = 3 };
+enum PairEpi : int { EPI_GLU = 0, EPI_GLU_AUX = 1, EPI_DGLU = 2, EPI_GRAD = 3, EPI_GLU_PART = 4, EPI_DGLU_PART = 5 };
 enum GateAct : int { GATE_SWIGLU = 0, GATE_GEGLU_TANH = 1 };
 
 constexpr int kPairThreads = (kEpiWarp0 + 8) * 32;
@@ -35,13 +37,15 @@ constexpr int kPairBars = 2 * 12 + 6 + 16;        // at most 12 stages; 16: two 
 constexpr uint32_t kPairBarBytes = 8u * (uint32_t)kPairBars;
 
 // bytes of one 32 x 32 block of a type, and of one epilogue warp's blocks: GLU and GRAD two in turn,
-// GLU_AUX one of each of h, g and u, DGLU two pairs (g and u, overwritten by dg and du)
+// GLU_AUX one of each of h, g and u, GLU_PART one of g and u, DGLU two pairs (g and u, overwritten by
+// dg and du)
 __host__ __device__ constexpr uint32_t pair_block_bytes(int out) { return out == DT_F32 ? 4096u : 2048u; }
 __host__ __device__ constexpr uint32_t pair_warp_staging(int epi, int out) {
   return pair_block_bytes(out) * (epi == EPI_GLU_AUX ? 3u : epi == EPI_DGLU ? 4u : 2u);
 }
 __host__ __device__ constexpr bool pair_a_mn(int epi) { return epi == EPI_GRAD; }
-__host__ __device__ constexpr bool pair_b_mn(int epi) { return epi == EPI_DGLU || epi == EPI_GRAD; }
+__host__ __device__ constexpr bool pair_b_mn(int epi) { return epi == EPI_DGLU || epi == EPI_GRAD || epi == EPI_DGLU_PART; }
+__host__ __device__ constexpr bool pair_glu(int epi) { return epi == EPI_GLU || epi == EPI_GLU_AUX || epi == EPI_GLU_PART; }
 
 // σ(y) = 1/(1 + e^(-y)); e^(-y) and the reciprocal on the special-function unit (relative errors
 // near 2^-22), saturating to 0 and 1
@@ -162,16 +166,17 @@ __device__ __forceinline__ void load_res32(float (&r)[32], const void* base, lon
 
 // Tensor maps: tmA, tmB operands (GLU: tmB gate rows, tmB2 up rows).  tm0..tm3 the epilogue's:
 //   GLU      tm0 h            GLU_AUX  tm0 h, tm1 g, tm2 u
-//   DGLU     tm0 g, tm1 u (loads), tm2 dg, tm3 du        GRAD  tm0 y (or the workspace)
-// p.M is the number of output rows (GRAD with splits: rows of one split, padded to whole tiles), p.N
-// its columns; columns from p.n_tma on (a ragged end below 16 bytes) are stored one by one.
+//   DGLU     tm0 g, tm1 u (loads), tm2 dg, tm3 du        GRAD, *_PART  tm0 y (or the workspace)
+// p.M is the number of output rows, p.N its columns; columns from p.n_tma on (a ragged end below 16
+// bytes) are stored one by one.  In a workspace p.N is the padded width of one partial result (of g,
+// which u follows, for GLU_PART), and p.split_rows ≥ p.M the rows of one split, a multiple of 32.
 template <int EPI, int ACT, int OUT>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fl_pair_tcgen05(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tm0,
                     const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2,
                     const __grid_constant__ CUtensorMap tm3, const __grid_constant__ KParams p) {
-  constexpr bool GLU = EPI == EPI_GLU || EPI == EPI_GLU_AUX;
+  constexpr bool GLU = pair_glu(EPI);
   constexpr bool A_MN = pair_a_mn(EPI), B_MN = pair_b_mn(EPI);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         } else {
           if (acc_any) tmem_wait_ld();
           float v[32];
-          if constexpr (GLU) {
+          if constexpr (EPI == EPI_GLU || EPI == EPI_GLU_AUX) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               float slope;
@@ -423,10 +428,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               for (int j = 0; j < 32; ++j) v[j] *= p.scale;
             }
           }
-          // the buffer's last store has read it (GLU_AUX: one buffer of three tiles; else two in turn)
-          const uint32_t sv = EPI == EPI_GLU_AUX ? stg : stg + (blk & 1u) * pair_block_bytes(OUT);
+          // the buffer's last store has read it (GLU_AUX, GLU_PART: one buffer of all tiles; else two in turn)
+          constexpr bool ONE = EPI == EPI_GLU_AUX || EPI == EPI_GLU_PART;
+          const uint32_t sv = ONE ? stg : stg + (blk & 1u) * pair_block_bytes(OUT);
           if (lane == 0) {
-            if constexpr (EPI == EPI_GLU_AUX) bulk_wait_group_read<0>();
+            if constexpr (ONE) bulk_wait_group_read<0>();
             else bulk_wait_group_read<1>();
           }
           __syncwarp();
@@ -435,6 +441,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ga[j]);
             put_block<OUT>(sv + 2048u, lane, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(gu[j]);
+            put_block<OUT>(sv + 4096u, lane, v);
+          } else if constexpr (EPI == EPI_GLU_PART) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(gu[j]);
             put_block<OUT>(sv + 4096u, lane, v);
@@ -447,8 +457,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (n0 < p.n_tma) {
-              tma_store_2d(&tm0, sv, n0, itm.split * p.split_rows + row0);
+            if (n0 < p.n_tma && (p.split_rows == 0 || row0 < p.split_rows)) {
+              const int r = itm.split * p.split_rows + row0;
+              tma_store_2d(&tm0, sv, n0, r);
+              if constexpr (EPI == EPI_GLU_PART) tma_store_2d(&tm0, sv + 4096u, p.N + n0, r);
               if constexpr (EPI == EPI_GLU_AUX) {
                 tma_store_2d(&tm1, sv + 2048u, n0, row0);
                 tma_store_2d(&tm2, sv + 4096u, n0, row0);
@@ -489,66 +501,126 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
 }
 
-// y[m,n] = (Σ_s ws[s][m][n] + residual[m,n])·scale over the S fp32 partial tiles, in split order.
-// A thread takes four columns of a row; rows of the workspace are 16-byte aligned.
-struct GradReduceArgs {
+// ---------------------------------------------------------------- after K splits
+// Σ_s ws[s] of four columns, in split order; the loads of eight splits are in flight together.
+__device__ __forceinline__ float4 sum_splits(const float* w, long long split_stride, int splits) {
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < splits; s0 += 8) {
+    float4 t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      t[k] = s0 + k < splits ? __ldcg(reinterpret_cast<const float4*>(w + (long long)(s0 + k) * split_stride))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a.x += t[k].x, a.y += t[k].y, a.z += t[k].z, a.w += t[k].w;
+  }
+  return a;
+}
+__device__ __forceinline__ float load_dt(const void* p, long long i, int dt) {
+  if (dt == DT_F32) return reinterpret_cast<const float*>(p)[i];
+  if (dt == DT_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(reinterpret_cast<const __half*>(p)[i]);
+}
+// four columns at element i (a multiple of four of a row that starts on 16 bytes), cnt of them inside
+__device__ __forceinline__ void load4_dt(float (&v)[4], const void* p, long long i, int dt, int cnt) {
+  if (cnt == 4 && dt == DT_F32) {
+    const float4 q = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+  } else if (cnt == 4) {
+    const uint2 q = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + i);
+    const float2 a = dt == DT_BF16 ? unpack2<DT_BF16>(q.x) : unpack2<DT_F16>(q.x);
+    const float2 b = dt == DT_BF16 ? unpack2<DT_BF16>(q.y) : unpack2<DT_F16>(q.y);
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = j < cnt ? load_dt(p, i + j, dt) : 0.0f;
+  }
+}
+__device__ __forceinline__ void store4_dt(void* p, long long i, int dt, int cnt, const float (&v)[4]) {
+  if (cnt == 4 && dt == DT_F32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+  } else if (cnt == 4) {
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + i) =
+        dt == DT_BF16 ? make_uint2(pack2<DT_BF16>(v[0], v[1]), pack2<DT_BF16>(v[2], v[3]))
+                      : make_uint2(pack2<DT_F16>(v[0], v[1]), pack2<DT_F16>(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= cnt) break;
+      if (dt == DT_F32) store_elem<DT_F32>(p, i + j, v[j]);
+      else if (dt == DT_BF16) store_elem<DT_BF16>(p, i + j, v[j]);
+      else store_elem<DT_F16>(p, i + j, v[j]);
+    }
+  }
+}
+
+struct FinishArgs {
   const float* ws;
-  long long split_stride, ld_ws;
+  long long split_stride, ld_ws, half;  // half: column of u in a row of the workspace
   int splits;
-  const void* residual;
+  const void* residual;  // GRAD
   long long ldr;
   int res_dtype;
   void* out;
   long long ldo;
   int out_dtype;
+  void* aux;  // [M, 2N] of out_dtype: written by GLU_AUX, read by DGLU
   long long M;
   int N, nvec;
   float scale;
 };
-static __global__ void __launch_bounds__(256) fl_grad_reduce_kernel(const GradReduceArgs P) {
+
+// The epilogue of a result in K splits; a thread takes four columns of a row.
+//   GRAD  y = (Σ + residual)·scale     GLU  h = act(Σg)·Σu, and g, u to aux when it is given
+//   DGLU  out = [Σ·u·act'(g), Σ·act(g)] with g, u from aux (out may be aux's own buffer)
+template <int EPI, int ACT>
+__global__ void __launch_bounds__(256) fl_split_finish_kernel(const FinishArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   const long long total = P.M * P.nvec;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
     const long long m = i / P.nvec;
     const int n0 = 4 * (int)(i - m * P.nvec);
-    const float4* w = reinterpret_cast<const float4*>(P.ws + m * P.ld_ws + n0);
-    float4 a = __ldcg(w);
-    for (int s0 = 1; s0 < P.splits; s0 += 4) {
-      float4 t[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        t[k] = s0 + k < P.splits ? __ldcg(w + (long long)(s0 + k) * (P.split_stride / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) a.x += t[k].x, a.y += t[k].y, a.z += t[k].z, a.w += t[k].w;
-    }
-    float v[4] = {a.x, a.y, a.z, a.w};
     const int cnt = min(4, P.N - n0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j >= cnt) break;
+    const float* w = P.ws + m * P.ld_ws + n0;
+    const float4 a = sum_splits(w, P.split_stride, P.splits);
+    float v[4] = {a.x, a.y, a.z, a.w};
+    if constexpr (EPI == EPI_GRAD) {
       if (P.residual != nullptr) {
-        const long long o = m * P.ldr + n0 + j;
-        v[j] += P.res_dtype == DT_F32    ? reinterpret_cast<const float*>(P.residual)[o]
-                : P.res_dtype == DT_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(P.residual)[o])
-                                         : __half2float(reinterpret_cast<const __half*>(P.residual)[o]);
+        float r[4];
+        load4_dt(r, P.residual, m * P.ldr + n0, P.res_dtype, cnt);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += r[j];
       }
-      v[j] *= P.scale;
-    }
-    // (rows of y start on 16 bytes, so four whole columns are one store)
-    const long long o = m * P.ldo + n0;
-    if (cnt == 4 && P.out_dtype == DT_F32) {
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(P.out) + o) = make_float4(v[0], v[1], v[2], v[3]);
-    } else if (cnt == 4) {
-      const uint2 h = P.out_dtype == DT_BF16 ? make_uint2(pack2<DT_BF16>(v[0], v[1]), pack2<DT_BF16>(v[2], v[3]))
-                                             : make_uint2(pack2<DT_F16>(v[0], v[1]), pack2<DT_F16>(v[2], v[3]));
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(P.out) + o) = h;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] *= P.scale;
+      store4_dt(P.out, m * P.ldo + n0, P.out_dtype, cnt, v);
+    } else if constexpr (EPI == EPI_GLU) {
+      const float4 b = sum_splits(w + P.half, P.split_stride, P.splits);
+      const float u[4] = {b.x, b.y, b.z, b.w};
+      if (P.aux != nullptr) {
+        store4_dt(P.aux, m * 2 * P.N + n0, P.out_dtype, cnt, v);
+        store4_dt(P.aux, m * 2 * P.N + P.N + n0, P.out_dtype, cnt, u);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float slope;
+        v[j] = gate_f<ACT>(v[j], slope) * u[j];
+      }
+      store4_dt(P.out, m * P.ldo + n0, P.out_dtype, cnt, v);
     } else {
-      for (int j = 0; j < cnt; ++j) {
-        if (P.out_dtype == DT_F32) store_elem<DT_F32>(P.out, o + j, v[j]);
-        else if (P.out_dtype == DT_BF16) store_elem<DT_BF16>(P.out, o + j, v[j]);
-        else store_elem<DT_F16>(P.out, o + j, v[j]);
+      float g[4], u[4], dg[4];
+      load4_dt(g, P.aux, m * 2 * P.N + n0, P.out_dtype, cnt);
+      load4_dt(u, P.aux, m * 2 * P.N + P.N + n0, P.out_dtype, cnt);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float slope;
+        const float act = gate_f<ACT>(g[j], slope);
+        dg[j] = v[j] * u[j] * slope;
+        v[j] *= act;
       }
+      store4_dt(P.out, m * P.ldo + n0, P.out_dtype, cnt, dg);
+      store4_dt(P.out, m * P.ldo + P.N + n0, P.out_dtype, cnt, v);
     }
   }
 }

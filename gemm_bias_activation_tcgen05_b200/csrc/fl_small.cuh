@@ -16,9 +16,20 @@
 
 namespace fl {
 
-constexpr int kSmallWarps = 8;
-constexpr int kSmallUnroll = 4;   // steps of 32 k in flight
-constexpr int kSmallMaxRows = 32;
+#ifndef SMR
+#define SMR 16
+#endif
+#ifndef SW
+#define SW 8
+#endif
+#ifndef SU1
+#define SU1 8
+#define SU2 2
+#define SC1 2
+#define SC2 1
+#endif
+constexpr int kSmallWarps = SW;
+constexpr int kSmallMaxRows = SMR;
 
 struct SmallArgs {
   const void *x, *w;
@@ -60,22 +71,29 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT: blocks of 8 rows of x (M ≤ 8·NT)
-template <int ACT, int DT, int NT>
-__global__ void __launch_bounds__(kSmallWarps * 32, NT <= 2 ? 3 : 2) fl_glu_small_kernel(const SmallArgs P) {
-  constexpr int U = kSmallUnroll, W = kSmallWarps;
-  __shared__ float part[W][2][8][8 * NT + 1];  // [warp][gate, up][feature][row of x]
+// NT: blocks of 8 rows of x (M ≤ 8·NT); FT: blocks of 8 features a warp (and CTA) owns.
+template <int ACT, int DT, int NT, int FT, int U>
+__global__ void __launch_bounds__(kSmallWarps * 32, FT == 1 ? SC1 : SC2) fl_glu_small_kernel(const SmallArgs P) {
+  constexpr int W = kSmallWarps;
+  __shared__ float part[W][2][8 * FT][8 * NT + 1];  // [warp][gate, up][feature][row of x]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * 8;
-  const bool n_ok = n0 + g < P.N;
-  const uint16_t* wg = reinterpret_cast<const uint16_t*>(P.w) + (long long)(n0 + g) * P.ldw;
-  const uint16_t* wu = wg + (long long)P.N * P.ldw;
+  const int n0 = blockIdx.x * 8 * FT;
+  bool n_ok[FT];
+  const uint16_t *wg[FT], *wu[FT];
+#pragma unroll
+  for (int f = 0; f < FT; ++f) {
+    n_ok[f] = n0 + 8 * f + g < P.N;
+    wg[f] = reinterpret_cast<const uint16_t*>(P.w) + (long long)(n0 + 8 * f + g) * P.ldw;
+    wu[f] = wg[f] + (long long)P.N * P.ldw;
+  }
   const uint16_t* xr = reinterpret_cast<const uint16_t*>(P.x) + (long long)g * P.ldx;
-  float acc[NT][4];
+  float acc[FT][NT][4];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int f = 0; f < FT; ++f)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[f][j][i] = 0.0f;
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
 
@@ -83,12 +101,14 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT <= 2 ? 3 : 2) fl_glu_smal
   const int whole = P.K / (32 * U);  // groups of U whole steps
   for (int s = warp; s < whole; s += W) {
     const int k0 = s * 32 * U + 8 * t;
-    uint4 a[U], b[U], x[U][NT];
+    uint4 a[U][FT], b[U][FT], x[U][NT];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      a[u] = n_ok ? ldg_stream(wg + k0 + 32 * u) : zero;
-      b[u] = n_ok ? ldg_stream(wu + k0 + 32 * u) : zero;
-    }
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int f = 0; f < FT; ++f) {
+        a[u][f] = n_ok[f] ? ldg_stream(wg[f] + k0 + 32 * u) : zero;
+        b[u][f] = n_ok[f] ? ldg_stream(wu[f] + k0 + 32 * u) : zero;
+      }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -97,42 +117,54 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT <= 2 ? 3 : 2) fl_glu_smal
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        mma_16816<DT>(acc[j], a[u].x, b[u].x, a[u].y, b[u].y, x[u][j].x, x[u][j].y);
-        mma_16816<DT>(acc[j], a[u].z, b[u].z, a[u].w, b[u].w, x[u][j].z, x[u][j].w);
-      }
+      for (int f = 0; f < FT; ++f)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_16816<DT>(acc[f][j], a[u][f].x, b[u][f].x, a[u][f].y, b[u][f].y, x[u][j].x, x[u][j].y);
+          mma_16816<DT>(acc[f][j], a[u][f].z, b[u][f].z, a[u][f].w, b[u][f].w, x[u][j].z, x[u][j].w);
+        }
   }
   // the last steps, one at a time
+#pragma unroll 1
   for (int s = whole * U + warp; 32 * s < P.K; s += W) {
     const int k = 32 * s + 8 * t;
     const bool in = k + 8 <= P.K, some = k < P.K;
-    uint4 a = zero, b = zero;
-    if (n_ok && some) {
-      a = in ? ldg_stream(wg + k) : ldg_tail(wg, k, P.K);
-      b = in ? ldg_stream(wu + k) : ldg_tail(wu, k, P.K);
-    }
+    uint4 x[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      uint4 x = zero;
+      x[j] = zero;
       if (g + 8 * j < P.M && some) {
         const uint16_t* r = xr + (long long)(8 * j) * P.ldx;
-        x = in ? *reinterpret_cast<const uint4*>(r + k) : ldg_tail(r, k, P.K);
+        x[j] = in ? *reinterpret_cast<const uint4*>(r + k) : ldg_tail(r, k, P.K);
       }
-      mma_16816<DT>(acc[j], a.x, b.x, a.y, b.y, x.x, x.y);
-      mma_16816<DT>(acc[j], a.z, b.z, a.w, b.w, x.z, x.w);
+    }
+#pragma unroll
+    for (int f = 0; f < FT; ++f) {
+      uint4 a = zero, b = zero;
+      if (n_ok[f] && some) {
+        a = in ? ldg_stream(wg[f] + k) : ldg_tail(wg[f], k, P.K);
+        b = in ? ldg_stream(wu[f] + k) : ldg_tail(wu[f], k, P.K);
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        mma_16816<DT>(acc[f][j], a.x, b.x, a.y, b.y, x[j].x, x[j].y);
+        mma_16816<DT>(acc[f][j], a.z, b.z, a.w, b.w, x[j].z, x[j].w);
+      }
     }
   }
   // lane (g, t): gate and up of feature g and x's rows 8j + 2t, 8j + 2t + 1
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    part[warp][0][g][8 * j + 2 * t] = acc[j][0];
-    part[warp][0][g][8 * j + 2 * t + 1] = acc[j][1];
-    part[warp][1][g][8 * j + 2 * t] = acc[j][2];
-    part[warp][1][g][8 * j + 2 * t + 1] = acc[j][3];
-  }
+  for (int f = 0; f < FT; ++f)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      part[warp][0][8 * f + g][8 * j + 2 * t] = acc[f][j][0];
+      part[warp][0][8 * f + g][8 * j + 2 * t + 1] = acc[f][j][1];
+      part[warp][1][8 * f + g][8 * j + 2 * t] = acc[f][j][2];
+      part[warp][1][8 * f + g][8 * j + 2 * t + 1] = acc[f][j][3];
+    }
   __syncthreads();
-  for (int e = threadIdx.x; e < 8 * P.M; e += W * 32) {
-    const int f = e & 7, m = e >> 3;
+  for (int e = threadIdx.x; e < 8 * FT * P.M; e += W * 32) {
+    const int f = e % (8 * FT), m = e / (8 * FT);
     float vg = 0.0f, vu = 0.0f, slope;
 #pragma unroll
     for (int w = 0; w < W; ++w) vg += part[w][0][f][m], vu += part[w][1][f][m];

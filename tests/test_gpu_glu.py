@@ -142,6 +142,25 @@ def test_glu_aux(fl, M, N, K, kind, dtype):
     _glu(fl, M, N, K, kind, dtype, aux=True)
 
 
+SPLIT = [(40, 264, 4096), (64, 1000, 4000), (300, 520, 3000), (257, 64, 8192), (600, 136, 2049)]
+
+
+@pytest.mark.parametrize("M,N,K", SPLIT)
+def test_few_tiles_in_k_splits(fl, M, N, K):
+    """Shapes whose tiles leave most of the GPU idle: K is cut, and a second kernel does the epilogue."""
+    for kind, b_major in (("SWIGLU", 0), ("GEGLU_TANH_AUX", 0), ("DSWIGLU", 1)):
+        i = fl.fl_plan_preview(M, N, K, "bf16", kind=kind, b_major=b_major, lda=up8(K), ldb=up8(N if b_major else K))
+        assert i["split_k"] > 1 and i["launches_per_execute"] == 2, (kind, i)
+    _glu(fl, M, N, K)
+    _glu(fl, M, N - 3, K, dtype="f16")
+    _glu(fl, M, N, K, "GEGLU_TANH", aux=True)
+    _glu(fl, M, N, K, "SWIGLU", "f16", aux=True, pad=8)
+    _glu(fl, M, N, K, noalloc=True)
+    _dglu(fl, M, N, K)
+    _dglu(fl, M, N, K, "GEGLU_TANH", "f16", pad=8)
+    _dglu(fl, M, N, K, in_place=True)
+
+
 def test_glu_noalloc(fl):
     _glu(fl, 3, 264, 520, noalloc=True)
     _glu(fl, 300, 264, 520, aux=True, kind="GEGLU_TANH", noalloc=True)
