@@ -529,17 +529,19 @@ extern "C" fl_status fl_plan(fl_plan_t* out, int64_t M, int64_t N, int64_t K, in
   const int eo = esize(epi->out_dtype);
 
   if (cudaGetDevice(&p->device) != cudaSuccess) { delete p; return fail(FL_ERR_DEVICE, "fl_plan: no CUDA device"); }
-  cudaDeviceProp prop;
-  if (cudaGetDeviceProperties(&prop, p->device) != cudaSuccess) {
+  // (single attributes: the whole property structure took most of a millisecond)
+  int major = 0, minor = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, p->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, p->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&p->max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, p->device) != cudaSuccess) {
     delete p;
     return fail(FL_ERR_DEVICE, "fl_plan: cannot query the device");
   }
-  if (prop.major != 10) {
+  if (major != 10) {
     delete p;
-    return fail(FL_ERR_DEVICE, "fl_plan: needs an sm_100 (B200-class) GPU, found sm_%d%d", prop.major, prop.minor);
+    return fail(FL_ERR_DEVICE, "fl_plan: needs an sm_100 (B200-class) GPU, found sm_%d%d", major, minor);
   }
-  p->num_sms = prop.multiProcessorCount;
-  p->max_smem = (int)prop.sharedMemPerBlockOptin;
   fl_status st = get_encode();
   if (st != FL_OK) { delete p; return st; }
   if (pair_kind(epi->kind)) {

@@ -26,24 +26,29 @@ int epi_of(int kind) {
 }
 bool is_geglu(int kind) { return kind == FL_EPI_GEGLU_TANH_AUX || kind == FL_EPI_DGEGLU_TANH; }
 
-template <int EPI, int ACT>
-PairFn by_out(int out) {
-  return out == FL_BF16 ? &fl_pair_tcgen05<EPI, ACT, DT_BF16> : &fl_pair_tcgen05<EPI, ACT, DT_F16>;
+template <int EPI, int ACT, int OUT>
+PairFn by_atoms(int atoms) {
+  return atoms == 2 ? &fl_pair_tcgen05<EPI, ACT, OUT, 2> : &fl_pair_tcgen05<EPI, ACT, OUT, 1>;
 }
-PairFn pair_kernel(int kind, int out, bool split) {
+template <int EPI, int ACT>
+PairFn by_out(int out, int atoms) {
+  return out == FL_BF16 ? by_atoms<EPI, ACT, DT_BF16>(atoms) : by_atoms<EPI, ACT, DT_F16>(atoms);
+}
+PairFn pair_kernel(int kind, int out, bool split, int atoms) {
   const int epi = epi_of(kind);
   if (split) {
-    return epi == EPI_GRAD   ? &fl_pair_tcgen05<EPI_GRAD, GATE_SWIGLU, DT_F32>
-           : epi == EPI_DGLU ? &fl_pair_tcgen05<EPI_DGLU_PART, GATE_SWIGLU, DT_F32>
-                             : &fl_pair_tcgen05<EPI_GLU_PART, GATE_SWIGLU, DT_F32>;
+    return epi == EPI_GRAD   ? by_atoms<EPI_GRAD, GATE_SWIGLU, DT_F32>(atoms)
+           : epi == EPI_DGLU ? by_atoms<EPI_DGLU_PART, GATE_SWIGLU, DT_F32>(atoms)
+                             : by_atoms<EPI_GLU_PART, GATE_SWIGLU, DT_F32>(atoms);
   }
   switch (kind) {
-    case FL_EPI_SWIGLU: return by_out<EPI_GLU, GATE_SWIGLU>(out);
-    case FL_EPI_GEGLU_TANH_AUX: return by_out<EPI_GLU_AUX, GATE_GEGLU_TANH>(out);
-    case FL_EPI_SWIGLU_AUX: return by_out<EPI_GLU_AUX, GATE_SWIGLU>(out);
-    case FL_EPI_DGEGLU_TANH: return by_out<EPI_DGLU, GATE_GEGLU_TANH>(out);
-    case FL_EPI_DSWIGLU: return by_out<EPI_DGLU, GATE_SWIGLU>(out);
-    default: return out == FL_F32 ? &fl_pair_tcgen05<EPI_GRAD, GATE_SWIGLU, DT_F32> : by_out<EPI_GRAD, GATE_SWIGLU>(out);
+    case FL_EPI_SWIGLU: return by_out<EPI_GLU, GATE_SWIGLU>(out, atoms);
+    case FL_EPI_GEGLU_TANH_AUX: return by_out<EPI_GLU_AUX, GATE_GEGLU_TANH>(out, atoms);
+    case FL_EPI_SWIGLU_AUX: return by_out<EPI_GLU_AUX, GATE_SWIGLU>(out, atoms);
+    case FL_EPI_DGEGLU_TANH: return by_out<EPI_DGLU, GATE_GEGLU_TANH>(out, atoms);
+    case FL_EPI_DSWIGLU: return by_out<EPI_DGLU, GATE_SWIGLU>(out, atoms);
+    default:
+      return out == FL_F32 ? by_atoms<EPI_GRAD, GATE_SWIGLU, DT_F32>(atoms) : by_out<EPI_GRAD, GATE_SWIGLU>(out, atoms);
   }
 }
 void (*finish_kernel(int kind))(FinishArgs) {
@@ -61,16 +66,14 @@ int kernel_epi(const fl_plan_s* p) {
   if (p->split_k == 1 || epi == EPI_GRAD) return epi;
   return epi == EPI_DGLU ? EPI_DGLU_PART : EPI_GLU_PART;
 }
-int kernel_out(const fl_plan_s* p) { return p->split_k > 1 ? FL_F32 : p->epi.out_dtype; }
-
 // Shared memory of the tile kernel: the ring, the epilogue warps' blocks, the barriers.
 struct PairLayout {
   uint32_t stage, staging, bar_off, total;
 };
 PairLayout pair_layout(const fl_plan_s* p) {
   PairLayout L;
-  L.stage = kPairABytes + (uint32_t)(p->mma_n / 2) * 128u;
-  L.staging = 8u * pair_warp_staging(kernel_epi(p), kernel_out(p));
+  L.stage = (uint32_t)p->k_atoms * (kPairABytes + (uint32_t)(p->mma_n / 2) * 128u);
+  L.staging = 8u * pair_warp_staging(p->k_atoms);
   L.bar_off = (uint32_t)p->stages * L.stage + L.staging;
   L.total = L.bar_off + kPairBarBytes + 1024u;  // (the ring starts on the next 1024 bytes)
   return L;
@@ -147,13 +150,27 @@ fl_status fl::host::pair_config(fl_plan_s* p, bool no_workspace) {
   p->out_tile_n = glu ? p->mma_n / 2 : p->mma_n;
   p->tiles_a = (int)cdiv(p->M, 256);
   p->tiles_b = (int)cdiv(p->N, p->out_tile_n);
+  // 128-deep stages where a unit's K loop is long enough to gain from them (see fl_pair.cuh).  From 8
+  // blocks on they measured no slower in any kind but the backward through the gate, whose epilogue
+  // then has one pair of g, u buffers a warp: about 2.6 us more a 256-wide tile (1.4 a 128-wide one),
+  // which shows in the last round, and in every round that is shorter than the epilogue, against 0.03
+  // (0.08) us less a block of 64.
+  const int kb = p->num_kb / p->split_k;
+  if (kernel_epi(p) == EPI_DGLU) {
+    const int64_t rounds = cdiv(cdiv(p->M, 256) * cdiv(p->N, p->mma_n), P);
+    const bool wide = p->mma_n == 256;
+    p->k_atoms = (rounds == 1 || kb >= 20) && (double)rounds * kb * (wide ? 0.03 : 0.08) > (wide ? 2.6 : 1.4) ? 2 : 1;
+  } else {
+    p->k_atoms = kb >= 8 ? 2 : 1;
+  }
+  p->num_kb = (int)cdiv(p->K, p->k_atoms * kPairBk);
   p->stages = 0;
   const PairLayout none = pair_layout(p);
   p->stages = (int)std::min<int64_t>(12, std::max<int64_t>(0, (int64_t)p->max_smem - none.total) / none.stage);
   if (p->stages < 2) return fail(FL_ERR_UNSUPPORTED, "fl_plan: shared memory too small");
   p->smem = (int)pair_layout(p).total;
   p->grid = (int)(2 * std::min<int64_t>((int64_t)p->tiles_a * p->tiles_b * p->split_k, P));
-  p->kernel = reinterpret_cast<const void*>(pair_kernel(p->epi.kind, p->epi.out_dtype, p->split_k > 1));
+  p->kernel = reinterpret_cast<const void*>(pair_kernel(p->epi.kind, p->epi.out_dtype, p->split_k > 1, p->k_atoms));
   p->launches = p->split_k > 1 ? 2 : 1;
   return FL_OK;
 }
@@ -191,6 +208,7 @@ fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, voi
   k.out_tile_n = p->out_tile_n;
   k.b_boxes = p->mma_n / 128;  // 64-column boxes of this CTA's half of an MN-major B
   k.stage_bytes = k.stage_stride = L.stage;
+  k.b_atom_bytes = (uint32_t)(p->mma_n / 2) * 128u;
   const uint32_t fmt = p->dtype == FL_BF16 ? 1u : 0u;
   k.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(pair_a_mn(epi) ? 1 : 0) << 15) |
             ((uint32_t)(pair_b_mn(epi) ? 1 : 0) << 16) | ((uint32_t)(p->mma_n >> 3) << 17) | ((256u >> 4) << 24);
@@ -215,11 +233,12 @@ fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, voi
   for (CUtensorMap* m : {&mA, &mB, &mB2, &m0, &m1, &m2, &m3}) memset(m, 0, sizeof(*m));
   fl_status st = FL_OK;
   if (K > 0) {
-    st = pair_a_mn(epi) ? make_map(&mA, A, p->dtype, M, K, (uint64_t)e.lda * es, 64, kPairBk)
+    const uint32_t depth = (uint32_t)(p->k_atoms * kPairBk);
+    st = pair_a_mn(epi) ? make_map(&mA, A, p->dtype, M, K, (uint64_t)e.lda * es, 64, depth)
                         : make_map(&mA, A, p->dtype, K, M, (uint64_t)e.lda * es, 64, 128);
     if (st) return st;
     if (pair_b_mn(epi)) {
-      st = make_map(&mB, W, p->dtype, N, K, (uint64_t)e.ldb * es, 64, kPairBk);
+      st = make_map(&mB, W, p->dtype, N, K, (uint64_t)e.ldb * es, 64, depth);
     } else {
       st = make_map(&mB, W, p->dtype, K, N, (uint64_t)e.ldb * es, 64, (uint32_t)p->out_tile_n);
       if (st) return st;

@@ -16,9 +16,15 @@
 //
 // Roles (320 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM allocator and (rank 0 of
 // the pair) UMMA issuer, warps 2..9 epilogue, two per TMEM lane quarter, each with half of the
-// tile's columns in blocks of 32.  Two accumulators, so that a tile's epilogue runs under the next
-// tile's products.  Stages are 64 deep in K: 32 KB a CTA, which leaves up to 64 KB for the epilogue's
-// tiles, which come and go by TMA (32 rows x 32 columns a block).
+// tile's columns in blocks of 32, which come and go by TMA.  Two accumulators, so that a tile's
+// epilogue runs under the next tile's products.
+//
+// Stages are ATOMS x 64 deep in K.  Each hand-over of a stage costs the tensor pipe some 40 clocks, so
+// 128-deep stages (64 KB a CTA, three of them) run long K loops faster: weight gradient 8192 x 4096 of
+// 4096 tokens 202.6 -> 185.6 us (1.48 PFLOP/s), SwiGLU backward 4096 x 8192 x 4096 224.7 -> 216.1.  They leave 4 KB of
+// shared memory for each epilogue warp; 64-deep ones (five or six) leave 8 KB, and with them the
+// epilogue, which bounds short K loops, waits less for its blocks: SwiGLU backward
+// 2048 x 2048 of 256 deep 13.5 us with 128-deep stages, 11.5 with 64-deep ones.
 //
 // Every wait is bounded; on expiry the kernel records an error code and unwinds.
 #pragma once
@@ -30,19 +36,15 @@ enum PairEpi : int { EPI_GLU = 0, EPI_GLU_AUX = 1, EPI_DGLU = 2, EPI_GRAD = 3, E
 enum GateAct : int { GATE_SWIGLU = 0, GATE_GEGLU_TANH = 1 };
 
 constexpr int kPairThreads = (kEpiWarp0 + 8) * 32;
-constexpr int kPairBk = 64;                       // K elements of a stage
-constexpr uint32_t kPairABytes = 128u * 128u;     // A: this CTA's 128 rows x 64
-constexpr uint32_t kPairBox = 64u * 128u;         // one MN-major box: 64 columns x 64 K rows
+constexpr int kPairBk = 64;                       // K elements of an atom (128 bytes of a K-major row)
+constexpr uint32_t kPairABytes = 128u * 128u;     // A: an atom of this CTA's 128 rows
+constexpr uint32_t kPairBox = 64u * 128u;         // an MN-major box of 64 columns x 64 K rows
 constexpr int kPairBars = 2 * 12 + 6 + 16;        // at most 12 stages; 16: two per epilogue warp
 constexpr uint32_t kPairBarBytes = 8u * (uint32_t)kPairBars;
 
-// bytes of one 32 x 32 block of a type, and of one epilogue warp's blocks: GLU and GRAD two in turn,
-// GLU_AUX one of each of h, g and u, GLU_PART one of g and u, DGLU two pairs (g and u, overwritten by
-// dg and du)
+// bytes of one 32 x 32 block of a type, and of the blocks of one epilogue warp
 __host__ __device__ constexpr uint32_t pair_block_bytes(int out) { return out == DT_F32 ? 4096u : 2048u; }
-__host__ __device__ constexpr uint32_t pair_warp_staging(int epi, int out) {
-  return pair_block_bytes(out) * (epi == EPI_GLU_AUX ? 3u : epi == EPI_DGLU ? 4u : 2u);
-}
+__host__ __device__ constexpr uint32_t pair_warp_staging(int atoms) { return atoms == 1 ? 8192u : 4096u; }
 __host__ __device__ constexpr bool pair_a_mn(int epi) { return epi == EPI_GRAD; }
 __host__ __device__ constexpr bool pair_b_mn(int epi) { return epi == EPI_DGLU || epi == EPI_GRAD || epi == EPI_DGLU_PART; }
 __host__ __device__ constexpr bool pair_glu(int epi) { return epi == EPI_GLU || epi == EPI_GLU_AUX || epi == EPI_GLU_PART; }
@@ -170,7 +172,7 @@ __device__ __forceinline__ void load_res32(float (&r)[32], const void* base, lon
 // p.M is the number of output rows, p.N its columns; columns from p.n_tma on (a ragged end below 16
 // bytes) are stored one by one.  In a workspace p.N is the padded width of one partial result (of g,
 // which u follows, for GLU_PART), and p.split_rows ≥ p.M the rows of one split, a multiple of 32.
-template <int EPI, int ACT, int OUT>
+template <int EPI, int ACT, int OUT, int ATOMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fl_pair_tcgen05(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tm0,
@@ -243,20 +245,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           const int s = (int)rs.s;
           if (!wait_bounded(empty_bar(s), rs.ph ^ 1u, p)) { ok = false; break; }
           const uint32_t sa = smem_base + (uint32_t)s * p.stage_stride;
-          const uint32_t sb = sa + kPairABytes;
+          const uint32_t sb = sa + ATOMS * kPairABytes;
           const uint32_t fb = mapa_shared(full_bar(s), 0);  // both CTAs' bytes complete on the leader's barrier
           if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2u * p.stage_bytes);
-          const int k0 = kb * kPairBk;
+          const int k0 = kb * ATOMS * kPairBk;
+          // (MN-major boxes span the stage's depth, K-major ones an atom)
           if constexpr (A_MN) {
             tma_load_2d_pair(sa, &tmA, fb, a_row, k0);
-            tma_load_2d_pair(sa + kPairBox, &tmA, fb, a_row + 64, k0);
+            tma_load_2d_pair(sa + ATOMS * kPairBox, &tmA, fb, a_row + 64, k0);
           } else {
-            tma_load_2d_pair(sa, &tmA, fb, k0, a_row);
+#pragma unroll
+            for (int a = 0; a < ATOMS; ++a) tma_load_2d_pair(sa + a * kPairABytes, &tmA, fb, k0 + a * kPairBk, a_row);
           }
           if constexpr (B_MN) {
-            for (int i = 0; i < p.b_boxes; ++i) tma_load_2d_pair(sb + (uint32_t)i * kPairBox, mb, fb, b_row + 64 * i, k0);
+            for (int i = 0; i < p.b_boxes; ++i)
+              tma_load_2d_pair(sb + (uint32_t)i * ATOMS * kPairBox, mb, fb, b_row + 64 * i, k0);
           } else {
-            tma_load_2d_pair(sb, mb, fb, k0, b_row);
+#pragma unroll
+            for (int a = 0; a < ATOMS; ++a)
+              tma_load_2d_pair(sb + (uint32_t)a * p.b_atom_bytes, mb, fb, k0 + a * kPairBk, b_row);
           }
         }
       }
@@ -271,11 +278,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     // ================================================================ UMMA issuer (rank 0 for both CTAs)
     if (lane == 0 && rank == 0) {
-      const uint64_t da0 = sdesc_sw128(smem_base, A_MN ? kPairBox : 16u, 1024);
-      const uint64_t db0 = sdesc_sw128(smem_base + kPairABytes, B_MN ? kPairBox : 16u, 1024);
+      const uint64_t da0 = sdesc_sw128(smem_base, A_MN ? ATOMS * kPairBox : 16u, 1024);
+      const uint64_t db0 = sdesc_sw128(smem_base + ATOMS * kPairABytes, B_MN ? ATOMS * kPairBox : 16u, 1024);
       const uint64_t stage_step = p.stage_stride >> 4;
-      // a UMMA step is 16 deep: 32 bytes along a K-major row, 16 K rows of 128 bytes in an MN-major box
-      constexpr uint32_t ak = (A_MN ? 2048u : 32u) >> 4, bk = (B_MN ? 2048u : 32u) >> 4;
+      // a UMMA step is 16 deep: 32 bytes along a K-major row of an atom, 16 K rows of 128 bytes in an
+      // MN-major box (start-address offsets in 16-byte units)
+      constexpr int STEPS = ATOMS * kPairBk / 16;
+      uint32_t ao[STEPS], bo[STEPS];
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) {
+        ao[k] = A_MN ? k * 128u : (k >> 2) * (kPairABytes >> 4) + (k & 3) * 2u;
+        bo[k] = B_MN ? k * 128u : (k >> 2) * (p.b_atom_bytes >> 4) + (k & 3) * 2u;
+      }
       const uint32_t idesc = p.idesc;
       uint32_t local = 0;
       StageRing rs;
@@ -293,8 +307,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           const uint64_t da = da0 + (uint64_t)s * stage_step;
           const uint64_t db = db0 + (uint64_t)s * stage_step;
 #pragma unroll
-          for (int k = 0; k < kPairBk / 16; ++k)
-            umma_f16_pair(d_tmem, da + k * ak, db + k * bk, idesc, (kb > itm.kb0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < STEPS; ++k)
+            umma_f16_pair(d_tmem, da + ao[k], db + bo[k], idesc, (kb > itm.kb0 || k > 0) ? 1u : 0u);
           umma_commit_pair_both(empty_bar(s));
           issued = true;
         }
@@ -319,12 +333,31 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int half_cols = p.out_tile_n >> 1;
     const int c_begin = (ew >> 2) * half_cols;
     const int nblk = half_cols / 32;
-    const uint32_t stg = smem_base + p.staging_off + (uint32_t)ew * pair_warp_staging(EPI, OUT);
+    const uint32_t stg = smem_base + p.staging_off + (uint32_t)ew * pair_warp_staging(ATOMS);
     uint32_t local = 0;
+    // Blocks leave through SLOTS block buffers in turn: `emit` waits until the store that used the
+    // next one has read it, then fills and stores it.
+    constexpr int SLOTS = (int)(pair_warp_staging(ATOMS) / pair_block_bytes(OUT));
+    uint32_t slot_at = 0;
+    auto emit = [&](const CUtensorMap* map, int x, int y, bool inside, const float (&v)[32]) {
+      if (lane == 0) bulk_wait_group_read<SLOTS - 1>();
+      __syncwarp();
+      const uint32_t at = stg + slot_at * pair_block_bytes(OUT);
+      put_block<OUT>(at, lane, v);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (inside) tma_store_2d(map, at, x, y);
+        bulk_commit_group();
+      }
+      slot_at = slot_at + 1 == (uint32_t)SLOTS ? 0u : slot_at + 1;
+    };
     uint32_t blk = 0;  // blocks this warp has begun (DGLU: the g, u tiles alternate between two buffers)
     bool ok = true;
     PairItem itm;
-    // DGLU: lane 0 sends for the g and u tiles of block b of an item into buffer `to`
+    // DGLU: g, u tiles arrive in, and dg, du leave from, GU pairs of buffers in turn; lane 0 sends for
+    // those of block b of an item into pair `to`
+    constexpr uint32_t GU = pair_warp_staging(ATOMS) / 4096u;
     auto fetch_gu = [&](const PairItem& w, int b, uint32_t to) {
       const int n0 = w.tb * p.out_tile_n + c_begin + 32 * b, r0 = w.ta * 256 + (int)rank * 128 + q * 32;
       mbar_arrive_expect_tx(aux_bar(ew, (int)to), 4096u);
@@ -336,7 +369,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if constexpr (EPI == EPI_DGLU) {
       if (more) {
         if (lane == 0) fetch_gu(itm, 0, 0);
-        fetched = 1;
+        fetched = 1;  // (the others follow, GU − 1 blocks ahead of their use)
       }
     }
     while (more) {
@@ -364,20 +397,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           for (int j = 0; j < 32; ++j) ga[j] = gu[j] = 0u;
         }
         if constexpr (EPI == EPI_DGLU) {
-          const uint32_t slot = blk & 1u;
+          const uint32_t slot = blk % GU;
           const uint32_t sg = stg + slot * 4096u, su = sg + 2048u;
-          // the other buffer's stores have read it: send for the next block's tiles
           const bool last = b + 1 == nblk;
-          if (!last || have_next) {
-            if (lane == 0) {
-              bulk_wait_group_read<0>();
-              if (last) fetch_gu(nxt, 0, slot ^ 1u);
-              else fetch_gu(itm, b + 1, slot ^ 1u);
+          auto fetch_next = [&]() {
+            // (the other pair's stores, or this one's, have read it)
+            if (!last || have_next) {
+              if (lane == 0) {
+                bulk_wait_group_read<0>();
+                if (last) fetch_gu(nxt, 0, (blk + 1) % GU);
+                else fetch_gu(itm, b + 1, (blk + 1) % GU);
+              }
+              ++fetched;
             }
-            ++fetched;
-          }
+          };
+          if constexpr (GU > 1) fetch_next();
           if (acc_any) tmem_wait_ld();
-          if (!warp_wait_bounded(aux_bar(ew, (int)slot), (blk >> 1) & 1u, p, lane)) { ok = false; break; }
+          if (!warp_wait_bounded(aux_bar(ew, (int)slot), (blk / GU) & 1u, p, lane)) { ok = false; break; }
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t ag = blk16_addr(sg, lane, c), au = blk16_addr(su, lane, c);
@@ -405,16 +441,28 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             bulk_commit_group();
           }
+          if constexpr (GU == 1) fetch_next();
         } else {
           if (acc_any) tmem_wait_ld();
+          const bool inside = n0 < p.n_tma && (p.split_rows == 0 || row0 < p.split_rows);
+          const int row = itm.split * p.split_rows + row0;
           float v[32];
+          if constexpr (EPI == EPI_GLU_AUX || EPI == EPI_GLU_PART) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ga[j]);
+            emit(EPI == EPI_GLU_AUX ? &tm1 : &tm0, n0, row, inside, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(gu[j]);
+            if constexpr (EPI == EPI_GLU_AUX) emit(&tm2, n0, row, inside, v);
+            else emit(&tm0, p.N + n0, row, inside, v);
+          }
           if constexpr (EPI == EPI_GLU || EPI == EPI_GLU_AUX) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               float slope;
               v[j] = gate_f<ACT>(__uint_as_float(ga[j]), slope) * __uint_as_float(gu[j]);
             }
-          } else {
+          } else if constexpr (EPI != EPI_GLU_PART) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ga[j]);
             if (p.residual != nullptr && m_ok && n0 < p.N) {
@@ -428,45 +476,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               for (int j = 0; j < 32; ++j) v[j] *= p.scale;
             }
           }
-          // the buffer's last store has read it (GLU_AUX, GLU_PART: one buffer of all tiles; else two in turn)
-          constexpr bool ONE = EPI == EPI_GLU_AUX || EPI == EPI_GLU_PART;
-          const uint32_t sv = ONE ? stg : stg + (blk & 1u) * pair_block_bytes(OUT);
-          if (lane == 0) {
-            if constexpr (ONE) bulk_wait_group_read<0>();
-            else bulk_wait_group_read<1>();
-          }
-          __syncwarp();
-          put_block<OUT>(sv, lane, v);
-          if constexpr (EPI == EPI_GLU_AUX) {
+          if constexpr (EPI != EPI_GLU_PART) {
+            if ((EPI == EPI_GLU || EPI == EPI_GRAD) && n0 + 32 > p.n_tma && n0 < p.N && m_ok) {
+              // ragged row end: a TMA store writes whole 16-byte granules
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ga[j]);
-            put_block<OUT>(sv + 2048u, lane, v);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(gu[j]);
-            put_block<OUT>(sv + 4096u, lane, v);
-          } else if constexpr (EPI == EPI_GLU_PART) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(gu[j]);
-            put_block<OUT>(sv + 4096u, lane, v);
-          } else if (n0 + 32 > p.n_tma && n0 < p.N && m_ok) {
-            // ragged row end: a TMA store writes whole 16-byte granules
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (n0 + j >= p.n_tma && n0 + j < p.N) store_elem<OUT>(p.out, (long long)m * p.ldo + n0 + j, v[j]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (n0 < p.n_tma && (p.split_rows == 0 || row0 < p.split_rows)) {
-              const int r = itm.split * p.split_rows + row0;
-              tma_store_2d(&tm0, sv, n0, r);
-              if constexpr (EPI == EPI_GLU_PART) tma_store_2d(&tm0, sv + 4096u, p.N + n0, r);
-              if constexpr (EPI == EPI_GLU_AUX) {
-                tma_store_2d(&tm1, sv + 2048u, n0, row0);
-                tma_store_2d(&tm2, sv + 4096u, n0, row0);
-              }
+              for (int j = 0; j < 32; ++j)
+                if (n0 + j >= p.n_tma && n0 + j < p.N) store_elem<OUT>(p.out, (long long)m * p.ldo + n0 + j, v[j]);
             }
-            bulk_commit_group();
+            emit(&tm0, n0, row, inside, v);
           }
         }
         if (b + 1 == nblk) {
@@ -486,7 +503,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     if constexpr (EPI == EPI_DGLU) {
       // after a wait that gave up: no tile may still be on its way when the CTA leaves
-      for (uint32_t f = blk; f < fetched; ++f) (void)warp_wait_bounded(aux_bar(ew, (int)(f & 1u)), (f >> 1) & 1u, p, lane);
+      for (uint32_t f = blk; f < fetched; ++f) (void)warp_wait_bounded(aux_bar(ew, (int)(f % GU)), (f / GU) & 1u, p, lane);
     }
     if (lane == 0) bulk_wait_group<0>();
     __syncwarp();
