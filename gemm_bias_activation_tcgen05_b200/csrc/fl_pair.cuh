@@ -54,18 +54,20 @@ __host__ __device__ constexpr bool pair_glu(int epi) { return epi == EPI_GLU || 
 __device__ __forceinline__ float sigmoid_f(float y) { return rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * y)); }
 // The tanh GELU is x·σ(2c(x + 0.044715x³)), c = √(2/π), because (1 + tanh y)/2 = σ(2y): no
 // cancellation for negative x, so that both gates keep fp32 precision over their whole range.
-// act(x), and in `slope` act'(x) = σ + x·σ·(1 − σ)·y'(x)
+// act(x), and in `slope` act'(x) = σ + x·σ·(1 − σ)·y'(x).  In the second term x is held within ±200,
+// where 1 − σ or σ has long been 0: no 0·∞ for the largest values.
 template <int ACT>
 __device__ __forceinline__ float gate_f(float x, float& slope) {
+  const float xc = fminf(fmaxf(x, -200.0f), 200.0f);
   if constexpr (ACT == GATE_SWIGLU) {
     const float s = sigmoid_f(x);
-    slope = s * fmaf(x, 1.0f - s, 1.0f);
+    slope = s * fmaf(xc, 1.0f - s, 1.0f);
     return x * s;
   } else {
     constexpr float k = 2.0f * 0.79788456080286536f;
-    const float x2 = x * x;
-    const float s = sigmoid_f(k * x * fmaf(0.044715f, x2, 1.0f));
-    slope = s * fmaf(x * (1.0f - s), k * fmaf(3.0f * 0.044715f, x2, 1.0f), 1.0f);
+    const float x2 = xc * xc;
+    const float s = sigmoid_f(k * xc * fmaf(0.044715f, x2, 1.0f));
+    slope = s * fmaf(xc * (1.0f - s), k * fmaf(3.0f * 0.044715f, x2, 1.0f), 1.0f);
     return x * s;
   }
 }

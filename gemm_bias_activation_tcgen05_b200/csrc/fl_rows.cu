@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "fl_host.h"
 #include "fl_rows.cuh"
@@ -77,13 +78,13 @@ struct RowKernel {
   void (*fn)(Args);
   int threads, vecs, block;  // threads 0: the kernel for rows of any length
 };
-// The types that have kernels of their own: activations in one 16-bit type, with the residual
-// stream in the same type or in fp32.  Everything else runs on the untyped kernels.
-enum RowTypes { ROWS_ANY, ROWS_BF16, ROWS_F16, ROWS_BF16_F32, ROWS_F16_F32 };
+// The types that have kernels of their own: activations in one type, with the residual stream in
+// the same type or in fp32.  Everything else runs on the untyped kernels.
+enum RowTypes { ROWS_ANY, ROWS_BF16, ROWS_F16, ROWS_BF16_F32, ROWS_F16_F32, ROWS_F32 };
 RowTypes row_types(bool vec, int64_t M, int64_t N, int x, int s, int z) {
   // (the typed kernels count blocks of random numbers in 32 bits)
-  if (!vec || N % 8 != 0 || M * (N / 4) >= (1LL << 32) || x != z || x == FL_F32) return ROWS_ANY;
-  if (s == x) return x == FL_BF16 ? ROWS_BF16 : ROWS_F16;
+  if (!vec || N % 8 != 0 || M * (N / 4) >= (1LL << 32) || x != z) return ROWS_ANY;
+  if (s == x) return x == FL_BF16 ? ROWS_BF16 : x == FL_F16 ? ROWS_F16 : ROWS_F32;
   if (s == FL_F32) return x == FL_BF16 ? ROWS_BF16_F32 : ROWS_F16_F32;
   return ROWS_ANY;
 }
@@ -94,6 +95,7 @@ RowKernel<DropLnArgs> ln_of(RowTypes r) {
     case ROWS_F16: return {fl_dropout_ln_kernel<T, V, DT_F16, DT_F16, DT_F16>, T, V, ln_block(T)};
     case ROWS_BF16_F32: return {fl_dropout_ln_kernel<T, V, DT_BF16, DT_F32, DT_BF16>, T, V, ln_block(T)};
     case ROWS_F16_F32: return {fl_dropout_ln_kernel<T, V, DT_F16, DT_F32, DT_F16>, T, V, ln_block(T)};
+    case ROWS_F32: return {fl_dropout_ln_kernel<T, V, DT_F32, DT_F32, DT_F32>, T, V, ln_block(T)};
     default: return {fl_dropout_ln_kernel<T, V, ANY, ANY, ANY>, T, V, ln_block(T)};
   }
 }
@@ -104,6 +106,7 @@ RowKernel<DropLnBwdArgs> ln_bwd_of(RowTypes r) {
     case ROWS_F16: return {fl_dropout_ln_bwd_kernel<T, V, DT_F16, DT_F16, DT_F16>, T, V, ln_bwd_block(T)};
     case ROWS_BF16_F32: return {fl_dropout_ln_bwd_kernel<T, V, DT_BF16, DT_F32, DT_BF16>, T, V, ln_bwd_block(T)};
     case ROWS_F16_F32: return {fl_dropout_ln_bwd_kernel<T, V, DT_F16, DT_F32, DT_F16>, T, V, ln_bwd_block(T)};
+    case ROWS_F32: return {fl_dropout_ln_bwd_kernel<T, V, DT_F32, DT_F32, DT_F32>, T, V, ln_bwd_block(T)};
     default: return {fl_dropout_ln_bwd_kernel<T, V, ANY, ANY, ANY>, T, V, ln_bwd_block(T)};
   }
 }
@@ -118,21 +121,23 @@ RowKernel<DropLnArgs> ln_kernel(int64_t N, RowTypes r) {
   if (N <= 16384) return ln_of<1024, 2>(r);
   return {fl_dropout_ln_long_kernel, 0, 0, 1024};
 }
-// Backward: two vectors a thread, which measured 85.8 us on 8192 x 4096 bf16 against 99.4 for one
-// (and twice the threads): what a row costs beside its elements is spread over more of them.
+// Backward: two vectors a thread (what a row costs beside its elements is spread over both), four
+// where a CTA of 256 threads then still holds the row.
 RowKernel<DropLnBwdArgs> ln_bwd_kernel(int64_t N, RowTypes r) {
   if (N <= 512) return ln_bwd_of<32, 2>(r);
   if (N <= 1024) return ln_bwd_of<64, 2>(r);
   if (N <= 2048) return ln_bwd_of<128, 2>(r);
   if (N <= 4096) return ln_bwd_of<256, 2>(r);
-  if (N <= 8192) return ln_bwd_of<512, 2>(r);
-  if (N <= 16384) return ln_bwd_of<1024, 2>(r);
+  if (N <= 8192) return ln_bwd_of<256, 4>(r);
+  if (N <= 16384) return ln_bwd_of<512, 4>(r);
   return {fl_dropout_ln_bwd_long_kernel, 0, 0, 1024};
 }
 
 // Launch geometry of the backward pass: CTAs (each leaves one partial row of dγ and one of dβ)
-// and the pitch of those rows.  At most two CTAs per SM (one of 512 threads or more), the
-// residency the kernel is built for: more would only add partial rows.
+// and the pitch of those rows.  One CTA per SM: a second one would halve the registers of each thread,
+// and the loop, which then keeps fewer loads and draws under way, measured slower with it (8192 x 4096
+// bf16: 87.7 us with two CTAs of 121 registers a thread, 75.5 with one of 160), and would leave twice
+// as many partial rows.
 struct BwdGeom {
   RowKernel<DropLnBwdArgs> k;
   int grid, ws_ld;
@@ -142,21 +147,27 @@ BwdGeom bwd_geom(int64_t M, int64_t N, int sms, RowTypes r) {
   BwdGeom g;
   g.k = ln_bwd_kernel(N, r);
   const int64_t ctas = cdiv(M, g.k.threads == 0 ? 1 : g.k.block / g.k.threads);
-  g.grid = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)sms * (g.k.block >= 512 ? 1 : 2)));
+  g.grid = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)sms));
   g.ws_ld = (int)(cdiv(N, 8) * 8);
   g.bytes = (size_t)g.grid * 2 * (size_t)g.ws_ld * sizeof(float);
   return g;
 }
 
-// The ring of rows ahead: two slots of `slot` bytes, or one where two do not fit, or none for
-// rows that are read in place (but at least `least` bytes).  A ring that takes a CTA above 48 KB with the kernel's own arrays
+// Bytes of one slot of the ring of rows ahead.
+template <typename Args>
+size_t slot_bytes(const RowKernel<Args>& k, std::initializer_list<const Mat*> ops) {
+  if (k.threads == 0) return 0;
+  size_t words = 0;
+  for (const Mat* m : ops) words += row_words(*m, k.vecs * k.threads);
+  return 16 * words * (size_t)(k.block / k.threads);
+}
+// The ring: two slots of `slot` bytes, or one where two do not fit (but at least `least` bytes).  A ring that takes a CTA above 48 KB with the kernel's own arrays
 // needs the kernel's opt-in.
 template <typename Args>
 fl_status ring_of(const RowKernel<Args>& k, size_t slot, size_t least, Args* P, size_t* smem) {
   constexpr size_t kMost = 200 * 1024;  // of the 227 KB of a CTA; the kernels' own arrays take at most 17 KB
   P->ahead = kRowsAhead * slot <= kMost ? kRowsAhead : 1;
-  *smem = k.threads == 0 || !P->vec ? 0 : P->ahead * slot;
-  *smem = std::max(*smem, least);
+  *smem = std::max(P->ahead * slot, least);
   if (*smem > 24 * 1024)
     FL_CUDA(cudaFuncSetAttribute((const void*)k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost));
   return FL_OK;
@@ -195,6 +206,7 @@ extern "C" fl_status fl_dropout(const void* x, const void* residual, void* y, in
                             : types == ROWS_F16      ? fl_dropout_kernel<DT_F16, DT_F16>
                             : types == ROWS_BF16_F32 ? fl_dropout_kernel<DT_BF16, DT_F32>
                             : types == ROWS_F16_F32  ? fl_dropout_kernel<DT_F16, DT_F32>
+                            : types == ROWS_F32      ? fl_dropout_kernel<DT_F32, DT_F32>
                                                      : fl_dropout_kernel<ANY, ANY>;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   const cudaError_t err = launch_pdl_b(fn, dim3((unsigned)grid), 256u, s, P);
@@ -241,7 +253,7 @@ extern "C" fl_status fl_dropout_layernorm(const void* x, const void* residual, c
   const RowKernel<DropLnArgs> k = ln_kernel(N, row_types(P.vec, M, N, x_dtype, sum_dtype, z_dtype));
   const int64_t ctas = cdiv(M, k.threads == 0 ? 1 : k.block / k.threads);
   size_t smem = 0;
-  if ((st = ring_of(k, operand_bytes(P.x, k.vecs, k.block) + operand_bytes(P.r, k.vecs, k.block), 0, &P, &smem))) return st;
+  if ((st = ring_of(k, slot_bytes(k, {&P.x, &P.r}), 0, &P, &smem))) return st;
   int sms = 148, per_sm = 0;
   if ((st = num_sms(&sms))) return st;
   // one resident wave of CTAs that walk the rows: their rows ahead are then always in flight
@@ -314,9 +326,8 @@ extern "C" fl_status fl_dropout_layernorm_backward(
   P.ws_ld = g.ws_ld;
   P.param_dt = param_dtype;
   size_t smem = 0;
-  if ((st = ring_of(g.k, operand_bytes(P.dz, g.k.vecs, g.k.block) + operand_bytes(P.s, g.k.vecs, g.k.block) +
-                             operand_bytes(P.ds_in, g.k.vecs, g.k.block),
-                    g.k.threads == 0 || !P.ws ? 0 : ln_bwd_part_bytes(g.k.threads, g.k.vecs), &P, &smem)))
+  if ((st = ring_of(g.k, slot_bytes(g.k, {&P.dz, &P.s, &P.ds_in}),
+                    g.k.block == g.k.threads || g.k.threads == 0 || !P.ws ? 0 : ln_bwd_part_bytes(g.k.threads, g.k.vecs), &P, &smem)))
     return st;
   cudaError_t err = launch_pdl_smem(g.k.fn, dim3((unsigned)g.grid), (unsigned)g.k.block, smem, s, P);
   if (err != cudaSuccess) return fail(FL_ERR_CUDA, "%s: kernel launch: %s", who, cudaGetErrorString(err));

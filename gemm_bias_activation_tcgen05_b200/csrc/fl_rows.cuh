@@ -112,10 +112,11 @@ struct Mat {
   int dt;
 };
 // The kernels come in two forms.  The typed ones know their operands' types (template arguments
-// ≥ 0) and run on rows of whole 16-byte vectors only; the others take the types from the operands
-// and check every vector, for odd widths, unaligned rows and rarer mixes of types.  The checks and
-// type branches cost about a third of the instructions, which bound these kernels: 8192 x 4096 bf16
-// with a residual, dropout 53.7 us untyped, with LayerNorm 86.5, its backward 133.
+// ≥ 0) and run on rows of whole 16-byte vectors that start on 16 bytes; the others take the types from
+// the operands, accept rows that start anywhere, and check every vector.  The checks and type branches
+// cost about a third of the instructions, which bound these kernels: 8192 x 4096 bf16 with a residual,
+// dropout 53.7 us untyped, with LayerNorm 86.5, its backward 133, against 42.6, 60.5 and 103 typed (in
+// their first forms).
 constexpr int ANY = -1;
 template <int DT>
 __device__ __forceinline__ int dt_of(const Mat& t) {
@@ -162,38 +163,86 @@ __device__ __forceinline__ float load1(const void* p, long long i, int dt) {
   const uint16_t h = reinterpret_cast<const uint16_t*>(p)[i];
   return dt == DT_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
 }
-__device__ __forceinline__ void store1(void* p, long long i, int dt, float v) {
-  if (dt == DT_F32) reinterpret_cast<float*>(p)[i] = v;
-  else if (dt == DT_BF16) reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
-}
 // elements c0 .. c0 + cnt − 1 of a row one by one, zeros after them
 __device__ __forceinline__ void load_some8(float (&v)[8], const Mat& t, long long row, int c0, int cnt) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = i < cnt ? load1(t.p, row * t.ld + c0 + i, t.dt) : 0.0f;
 }
-// v into elements c0 .. c0 + cnt − 1; vec: all eight, as 16-byte stores
+// Eight elements that start `skew` bytes into the words w (three 16-byte words; 16-bit types need two).
+__device__ __forceinline__ Raw8 unskew(uint32_t (&w)[12], int skew) {
+  if (skew & 8) {
+#pragma unroll
+    for (int j = 0; j < 10; ++j) w[j] = w[j + 2];
+  }
+  if (skew & 4) {
+#pragma unroll
+    for (int j = 0; j < 9; ++j) w[j] = w[j + 1];
+  }
+  if (skew & 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+  }
+  return {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
+}
+// Elements c0 .. c0 + 7 of a row that starts anywhere, zeros from element cnt on: the 16-byte words
+// that hold them where these lie inside the operand (M rows of N), else one by one.
+__device__ __forceinline__ void gather8(float (&v)[8], const Mat& t, long long row, long long M, int N, int c0, int cnt) {
+  const int es = t.dt == DT_F32 ? 4 : 2;
+  const char* base = reinterpret_cast<const char*>(t.p);
+  const char* at = base + (row * t.ld + c0) * es;
+  const int skew = (int)(reinterpret_cast<uintptr_t>(at) & 15u);
+  const int words = es / 2 + (skew != 0);
+  const char* from = at - skew;
+  if (cnt < 8 || from < base || from + 16 * words > base + ((M - 1) * t.ld + N) * es) {
+    load_some8(v, t, row, c0, cnt);
+    return;
+  }
+  uint32_t w[12];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const uint4 q = j < words ? reinterpret_cast<const uint4*>(from)[j] : make_uint4(0u, 0u, 0u, 0u);
+    w[4 * j] = q.x, w[4 * j + 1] = q.y, w[4 * j + 2] = q.z, w[4 * j + 3] = q.w;
+  }
+  widen8(v, unskew(w, skew), t.dt);
+}
+// v into elements c0 .. c0 + cnt − 1.  vec: all eight, on 16 bytes.  Otherwise eight elements that
+// start anywhere go out as words where they can (16-bit types: a first half, three words and a last
+// half where the address is odd in words), fewer one by one.
 __device__ __forceinline__ void store8(const Mat& t, long long row, int c0, int cnt, bool vec, const float (&v)[8], int dt) {
-  if (vec) {
-    if (dt == DT_F32) {
-      float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(t.p) + row * t.ld + c0);
-      q[0] = make_float4(v[0], v[1], v[2], v[3]);
-      q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  const long long i0 = row * t.ld + c0;
+  if (dt == DT_F32) {
+    float* q = reinterpret_cast<float*>(t.p) + i0;
+    if (vec) {
+      reinterpret_cast<float4*>(q)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(q)[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-      uint4 q;
-      if (dt == DT_BF16) {
-        q = make_uint4(pack2<DT_BF16>(v[0], v[1]), pack2<DT_BF16>(v[2], v[3]), pack2<DT_BF16>(v[4], v[5]),
-                       pack2<DT_BF16>(v[6], v[7]));
-      } else {
-        q = make_uint4(pack2<DT_F16>(v[0], v[1]), pack2<DT_F16>(v[2], v[3]), pack2<DT_F16>(v[4], v[5]),
-                       pack2<DT_F16>(v[6], v[7]));
-      }
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(t.p) + row * t.ld + c0) = q;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < cnt) q[i] = v[i];
+    }
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = dt == DT_BF16 ? pack2<DT_BF16>(v[2 * j], v[2 * j + 1]) : pack2<DT_F16>(v[2 * j], v[2 * j + 1]);
+  uint16_t* q = reinterpret_cast<uint16_t*>(t.p) + i0;
+  if (vec) {
+    *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if (cnt == 8) {
+    if ((reinterpret_cast<uintptr_t>(q) & 2u) == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(q)[j] = w[j];
+    } else {
+      q[0] = (uint16_t)w[0];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) *reinterpret_cast<uint32_t*>(q + 1 + 2 * j) = __funnelshift_r(w[j], w[j + 1], 16);
+      q[7] = (uint16_t)(w[3] >> 16);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < cnt) store1(t.p, row * t.ld + c0 + i, dt, v[i]);
+      if (i < cnt) q[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
   }
 }
 // eight parameters of type dt from c0; `dflt` for a null pointer
@@ -204,7 +253,7 @@ __device__ __forceinline__ void load_param8(float (&v)[8], const void* p, int dt
   } else {
     const Mat t{const_cast<void*>(p), 0, dt};
     if (vec) widen8(v, load_raw8(t, 0, c0, dt), dt);
-    else load_some8(v, t, 0, c0, cnt);
+    else gather8(v, t, 0, 1, c0 + cnt, c0, cnt);
   }
 }
 
@@ -278,12 +327,12 @@ __global__ void __launch_bounds__(256, dropout_ctas(XT >= 0)) fl_dropout_kernel(
     if (P.d.on) w = draw8<!TYPED>((uint64_t)(row * groups + (c0 >> 2)), off, P.d);
     float x[8], r[8];
     if (vec) widen8(x, rx, xt);
-    else load_some8(x, P.x, row, c0, cnt);
+    else gather8(x, P.x, row, P.M, P.N, c0, cnt);
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = 0.0f;
     if (has_r) {
       if (vec) widen8(r, rr, yt);
-      else load_some8(r, P.r, row, c0, cnt);
+      else gather8(r, P.r, row, P.M, P.N, c0, cnt);
     }
     if (P.d.on) {
       add_dropped8(r, x, w, P.d);
@@ -299,12 +348,15 @@ __global__ void __launch_bounds__(256, dropout_ctas(XT >= 0)) fl_dropout_kernel(
 }
 
 // ---------------------------------------------------------------- sums over a row's threads
-// Sums of one or two values over the T threads that share a row, the same in every thread: a
-// butterfly in each warp, then the warps' sums in warp order.  `red` holds two sets of T/32
-// pairs, used in turn (`flip`), so that one barrier a call is enough: a warp writes a set again
-// only after the next call's barrier, which every reader of the set has passed its reads before.
+// Sums of one or two values over the threads that share a row, the same in every thread: a
+// butterfly in each warp, then the warps' sums in warp order.  `red` holds two sets of T/32 pairs,
+// used in turn (`flip`), so that one barrier a call is enough: a warp writes a set again only after the
+// next call's barrier, which every reader of the set has passed its reads before.
+__device__ __forceinline__ void row_barrier(int group, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
+}
 template <int T>
-__device__ __forceinline__ float2 row_sum2(float2 v, float2* red, int& flip, int group) {
+__device__ __forceinline__ float2 row_sum2(float2 v, float2* red, int& flip, int group, int t) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
@@ -312,8 +364,8 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* red, int& flip, int
     constexpr int W = T / 32;
     float2* set = red + flip * W;
     flip ^= 1;
-    if ((threadIdx.x & 31) == 0) set[(threadIdx.x % T) >> 5] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(T) : "memory");
+    if ((t & 31) == 0) set[t >> 5] = v;
+    row_barrier(group, T);
     v = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < W; i += 2) {
@@ -325,18 +377,20 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* red, int& flip, int
   return v;
 }
 template <int T>
-__device__ __forceinline__ float row_sum(float v, float2* red2, int& flip, int group) {
+__device__ __forceinline__ float row_sum(float v, float2* red2, int& flip, int group, int t) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (T > 32) {
     constexpr int W = T / 32;
     float* set = reinterpret_cast<float*>(red2 + flip * W);
     flip ^= 1;
-    if ((threadIdx.x & 31) == 0) set[(threadIdx.x % T) >> 5] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(T) : "memory");
+    if ((t & 31) == 0) set[t >> 5] = v;
+    row_barrier(group, T);
     float2 a = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < W; i += 2) a = add2(a, *reinterpret_cast<const float2*>(set + i));
+    for (int i = 0; i < W; i += 2) {
+      a = add2(a, *reinterpret_cast<const float2*>(set + i));
+    }
     v = a.x + a.y;
   }
   return v;
@@ -350,39 +404,95 @@ __device__ __forceinline__ float div_n(float a, float n, float inv) {
 }
 
 // ---------------------------------------------------------------- rows ahead in shared memory
-// A thread copies its own vectors of a row into its own slots of shared memory (cp.async, one
-// group a row) `ahead` rows before it needs them, and reads back only those, so that no barrier
-// stands between the copy and its use, and the bytes in flight cost no registers.  One ring slot
-// holds, for each operand, V·BLOCK 16-byte pieces (16-bit types) or two such planes (fp32).  The
-// ring has two slots, or one where two do not fit (fp32 rows of more than 8192 elements).
+// The 16-byte words of a row are copied to shared memory (cp.async, one group a row) `ahead` rows
+// before they are needed, so that the bytes in flight cost no registers.  The ring has two slots, or
+// one where two do not fit.  A slot holds for each operand and row group `row_words` words.
+//  * Typed: a thread copies its own vectors and reads back only those: no barrier stands between the
+//    copy and its use.
+//  * Untyped: the row may start anywhere.  The words that cover it are copied, the row's threads meet
+//    at a barrier, and a thread puts its eight elements together from the words they lie in.
 constexpr int kRowsAhead = 2;
 __device__ __forceinline__ void wait_row(int ahead) {
   if (ahead == kRowsAhead) cp_async_wait<kRowsAhead - 1>();
   else cp_async_wait<0>();
 }
-__host__ __device__ __forceinline__ uint32_t plane_bytes(int v, int block) { return (uint32_t)v * (uint32_t)block * 16u; }
-__host__ __device__ __forceinline__ uint32_t operand_bytes(const Mat& t, int v, int block) {
-  return t.p == nullptr ? 0u : plane_bytes(v, block) * (t.dt == DT_F32 ? 2u : 1u);
+// words of a row of `vectors` vectors of eight; two more for one that starts anywhere
+__host__ __device__ __forceinline__ uint32_t row_words(const Mat& t, int vectors) {
+  return t.p == nullptr ? 0u : (uint32_t)vectors * (t.dt == DT_F32 ? 2u : 1u) + 2u;
 }
-template <int V, int BLOCK>
-__device__ __forceinline__ void stage_vec(uint32_t dst, const Mat& t, long long row, int c0, int k, int dt) {
-  const char* src = reinterpret_cast<const char*>(t.p) + (row * t.ld + c0) * (dt == DT_F32 ? 4 : 2);
-  const uint32_t a = dst + (uint32_t)(k * BLOCK + threadIdx.x) * 16u;
-  cp_async_16(a, src, 16u);
-  if (dt == DT_F32) cp_async_16(a + plane_bytes(V, BLOCK), src + 16, 16u);
-}
-template <int V, int BLOCK>
-__device__ __forceinline__ void unstage_vec(float (&v)[8], uint32_t src, int dt, int k) {
-  const uint32_t a = src + (uint32_t)(k * BLOCK + threadIdx.x) * 16u;
-  const float4 q = ld_shared_f4(a);
-  Raw8 r;
-  r.a = make_uint4(__float_as_uint(q.x), __float_as_uint(q.y), __float_as_uint(q.z), __float_as_uint(q.w));
-  r.b = make_uint4(0u, 0u, 0u, 0u);
+
+// Typed: vector vi of a row to its place from `dst`; an fp32 vector's second half lies `vectors` words
+// behind its first.  The two halves share 32-byte sectors, so they go through the L1 cache: past it
+// each sector is fetched twice (LayerNorm of 4096 x 4096 fp32 with a residual: 71.0 us so, 46.7 with the
+// cache).  A line may outlive its data there when y is x's own buffer, but a row is read by its own
+// threads alone, before they write it.
+__device__ __forceinline__ void stage_vec(uint32_t dst, const Mat& t, long long row, int vi, int vectors, int dt) {
+  const char* src = reinterpret_cast<const char*>(t.p) + (row * t.ld + 8 * vi) * (dt == DT_F32 ? 4 : 2);
+  const uint32_t a = dst + (uint32_t)vi * 16u;
   if (dt == DT_F32) {
-    const float4 w = ld_shared_f4(a + plane_bytes(V, BLOCK));
-    r.b = make_uint4(__float_as_uint(w.x), __float_as_uint(w.y), __float_as_uint(w.z), __float_as_uint(w.w));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(a), "l"(src) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(a + (uint32_t)vectors * 16u), "l"(src + 16) : "memory");
+  } else {
+    cp_async_16(a, src, 16u);
   }
+}
+__device__ __forceinline__ uint4 ld_shared_w4(uint32_t a) {
+  const float4 q = ld_shared_f4(a);
+  return make_uint4(__float_as_uint(q.x), __float_as_uint(q.y), __float_as_uint(q.z), __float_as_uint(q.w));
+}
+__device__ __forceinline__ void unstage_vec(float (&v)[8], uint32_t src, int vi, int vectors, int dt) {
+  const uint32_t a = src + (uint32_t)vi * 16u;
+  Raw8 r;
+  r.a = ld_shared_w4(a);
+  r.b = make_uint4(0u, 0u, 0u, 0u);
+  if (dt == DT_F32) r.b = ld_shared_w4(a + (uint32_t)vectors * 16u);
   widen8(v, r, dt);
+}
+
+// Untyped: this thread's share (words t, t + threads, ...) of the words that cover row `row`.  A word
+// that reaches outside the operand (its first row may start, its last row end, inside a word) is put
+// together element by element.
+__device__ __forceinline__ void stage_row(uint32_t dst, const Mat& t, long long row, long long M, int N, int tid, int threads) {
+  const int es = t.dt == DT_F32 ? 4 : 2;
+  const char* base = reinterpret_cast<const char*>(t.p);
+  const char* begin = base + row * t.ld * es;
+  const char* end = begin + (long long)N * es;
+  const char* last = base + ((M - 1) * t.ld + N) * es;  // the operand's end
+  const int skew = (int)(reinterpret_cast<uintptr_t>(begin) & 15u);
+  const char* from = begin - skew;
+  const int words = (int)((skew + (long long)N * es + 15) >> 4);
+  for (int j = tid; j < words; j += threads) {
+    const char* src = from + 16LL * j;
+    const uint32_t to = dst + (uint32_t)j * 16u;
+    if (src >= base && src + 16 <= last) {
+      cp_async_16(to, src, 16u);
+    } else {
+      for (int e = 0; e < 16; e += es) {
+        if (src + e < begin || src + e >= end) continue;
+        if (es == 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + e), "r"(*reinterpret_cast<const uint32_t*>(src + e)) : "memory");
+        else asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + e), "h"(*reinterpret_cast<const uint16_t*>(src + e)) : "memory");
+      }
+    }
+  }
+}
+// eight elements from element 8·vi of a staged row, zeros from element cnt on
+__device__ __forceinline__ void unstage_row(float (&v)[8], uint32_t src, const Mat& t, long long row, int vi, int cnt) {
+  const int es = t.dt == DT_F32 ? 4 : 2;
+  const int skew = (int)((reinterpret_cast<uintptr_t>(t.p) + (unsigned long long)(row * t.ld * es)) & 15u);
+  const uint32_t a = src + (uint32_t)vi * (8u * (uint32_t)es);
+  uint32_t w[12];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    // (the word behind the vector only where the row is skewed; 16-bit types have no third word)
+    if (j == 0 || (j == 1 && (es == 4 || skew != 0)) || (j == 2 && es == 4 && skew != 0)) q = ld_shared_w4(a + 16u * j);
+    w[4 * j] = q.x, w[4 * j + 1] = q.y, w[4 * j + 2] = q.z, w[4 * j + 3] = q.w;
+  }
+  widen8(v, unskew(w, skew), t.dt);
+  if (cnt < 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < cnt ? v[i] : 0.0f;
+  }
 }
 
 // ---------------------------------------------------------------- dropout, residual, LayerNorm
@@ -399,42 +509,45 @@ struct DropLnArgs {
 
 // T threads hold a row, V vectors of eight each (N ≤ 8·V·T): the row is read once, stays in
 // registers through the mean, Σ(s − μ)² and the normalisation, and every output is written once.
-// A CTA holds max(1, 128/T) rows at a time and walks the rows a grid apart; γ and β stay in
-// registers (but for 1024 threads, which have 64 each).
+// A CTA holds max(1, 128/T) rows at a time and walks the rows a grid apart; γ and β stay in registers (but for 1024 threads, which have 64 each).
 __host__ __device__ constexpr int ln_block(int t) { return t < 128 ? 128 : t; }
 template <int T, int V, int XT, int ST, int ZT>
-__global__ void __launch_bounds__(ln_block(T), T <= 128 ? 4 : T == 256 ? 2 : 1) fl_dropout_ln_kernel(const DropLnArgs P) {
+__global__ void __launch_bounds__(ln_block(T), T <= 128 ? 4 : 1) fl_dropout_ln_kernel(const DropLnArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   constexpr bool TYPED = XT >= 0, HOIST = T < 1024;
-  constexpr int BLOCK = ln_block(T);
-  constexpr int R = BLOCK / T;
+  constexpr int R = ln_block(T) / T;
   extern __shared__ __align__(16) uint8_t ring_s[];
   __shared__ __align__(16) float2 red_s[R][2 * (T / 32)];
   const int xt = dt_of<XT>(P.x), st = ST >= 0 ? ST : (P.r.p != nullptr ? P.r.dt : P.s.dt), zt = dt_of<ZT>(P.z);
+  constexpr int threads = T, vectors = V * T;  // of a row
   const int group = threadIdx.x / T, t = threadIdx.x % T;
   int flip = 0;
   const DropOffset off = drop_offset(P.d);
   const long long groups = (P.N + 3) / 4;
   const float n_f = (float)P.N, inv_n = 1.0f / n_f;
   const long long m0 = (long long)blockIdx.x * R + group, step = (long long)gridDim.x * R;
-  const uint32_t ring = smem_u32(ring_s);
-  const uint32_t xb = operand_bytes(P.x, V, BLOCK), slot_bytes = xb + operand_bytes(P.r, V, BLOCK);
+  const uint32_t xw = row_words(P.x, vectors), rw = row_words(P.r, vectors);
+  const uint32_t slot_bytes = 16u * R * (xw + rw);
+  const uint32_t ring = smem_u32(ring_s), xo = 16u * group * xw, ro = 16u * (R * xw + group * rw);
   const bool has_r = P.r.p != nullptr;
   // elements of vector k inside the row (typed: 8 or none)
   auto count = [&](int k) {
-    const int left = P.N - 8 * (k * T + t);
+    const int left = P.N - 8 * (k * threads + t);
     return TYPED ? (left > 0 ? 8 : 0) : max(0, min(8, left));
   };
   auto prefetch = [&](long long m, uint32_t slot) {
-    if (m < P.M && (TYPED || P.vec)) {
+    if (m < P.M) {
+      if constexpr (TYPED) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c0 = 8 * (k * T + t);
-        if (count(k) == 8) {
-          stage_vec<V, BLOCK>(slot, P.x, m, c0, k, xt);
-          if (has_r) stage_vec<V, BLOCK>(slot + xb, P.r, m, c0, k, st);
+        for (int k = 0; k < V; ++k) {
+          if (count(k) == 0) continue;
+          stage_vec(slot + xo, P.x, m, k * threads + t, vectors, xt);
+          if (has_r) stage_vec(slot + ro, P.r, m, k * threads + t, vectors, st);
         }
+      } else {
+        stage_row(slot + xo, P.x, m, P.M, P.N, t, threads);
+        if (has_r) stage_row(slot + ro, P.r, m, P.M, P.N, t, threads);
       }
     }
     cp_async_commit();
@@ -442,7 +555,7 @@ __global__ void __launch_bounds__(ln_block(T), T <= 128 ? 4 : T == 256 ? 2 : 1) 
   for (int i = 0; i < P.ahead; ++i) prefetch(m0 + i * step, ring + i * slot_bytes);
   float gam[HOIST ? V : 1][8], bet[HOIST ? V : 1][8];
   auto params = [&](int k, float (&g)[8], float (&b)[8]) {
-    const int c0 = 8 * (k * T + t), cnt = count(k);
+    const int c0 = 8 * (k * threads + t), cnt = count(k);
     const bool vec = TYPED || (P.vec && cnt == 8);
     load_param8(g, P.gamma, P.param_dt, c0, cnt, vec, 1.0f);
     load_param8(b, P.beta, P.param_dt, c0, cnt, vec, 0.0f);
@@ -460,22 +573,22 @@ __global__ void __launch_bounds__(ln_block(T), T <= 128 ? 4 : T == 256 ? 2 : 1) 
     Draw8 w[V];
     if (P.d.on) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) w[k] = draw8<!TYPED>((uint64_t)(m * groups + 2 * (k * T + t)), off, P.d);
+      for (int k = 0; k < V; ++k) w[k] = draw8<!TYPED>((uint64_t)(m * groups + 2 * (k * threads + t)), off, P.d);
     }
-    wait_row(P.ahead);  // this row's copies have landed
+    wait_row(P.ahead);  // this thread's copies of the row have landed
+    if constexpr (!TYPED) row_barrier(group, threads);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c0 = 8 * (k * T + t), cnt = count(k);
+      const int vi = k * threads + t, cnt = count(k);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[k][i] = 0.0f;
       if (cnt == 0) continue;
-      const bool vec = TYPED || (P.vec && cnt == 8);
       float x[8];
-      if (vec) unstage_vec<V, BLOCK>(x, slot, xt, k);
-      else load_some8(x, P.x, m, c0, cnt);
+      if constexpr (TYPED) unstage_vec(x, slot + xo, vi, vectors, xt);
+      else unstage_row(x, slot + xo, P.x, m, vi, cnt);
       if (has_r) {
-        if (vec) unstage_vec<V, BLOCK>(s[k], slot + xb, st, k);
-        else load_some8(s[k], P.r, m, c0, cnt);
+        if constexpr (TYPED) unstage_vec(s[k], slot + ro, vi, vectors, st);
+        else unstage_row(s[k], slot + ro, P.r, m, vi, cnt);
       }
       if (P.d.on) {
         add_dropped8(s[k], x, w[k], P.d);
@@ -483,14 +596,18 @@ __global__ void __launch_bounds__(ln_block(T), T <= 128 ? 4 : T == 256 ? 2 : 1) 
 #pragma unroll
         for (int j = 0; j < 4; ++j) put_pair(s[k], j, add2(pair_of(s[k], j), pair_of(x, j)));
       }
-      if (P.s.p != nullptr) store8(P.s, m, c0, cnt, vec, s[k], st);
-      // (elements past the row were loaded as zeros, and zeros they stay)
+      if (P.s.p != nullptr) store8(P.s, m, 8 * vi, cnt, TYPED || (P.vec && cnt == 8), s[k], st);
+      // (elements past the row are zeros, and zeros they stay)
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum2 = add2(sum2, pair_of(s[k], j));
     }
-    prefetch(m + P.ahead * step, slot);  // (the slot's values are in registers)
+    if constexpr (TYPED) prefetch(m + P.ahead * step, slot);  // (the slot's values are in registers)
+    const float mean = div_n(row_sum<T>(sum2.x + sum2.y, red_s[group], flip, group, t), n_f, inv_n);
+    if constexpr (!TYPED) {
+      // every thread's values are in registers (T = 32: the butterfly above joined the warp)
+      prefetch(m + P.ahead * step, slot);
+    }
     at = at + 1 == P.ahead ? 0 : at + 1;
-    const float mean = div_n(row_sum<T>(sum2.x + sum2.y, red_s[group], flip, group), n_f, inv_n);
     float2 q2 = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -504,11 +621,12 @@ __global__ void __launch_bounds__(ln_block(T), T <= 128 ? 4 : T == 256 ? 2 : 1) 
         q2 = fma2(d, d, q2);
       }
     }
-    const float rstd = 1.0f / sqrtf(div_n(row_sum<T>(q2.x + q2.y, red_s[group], flip, group), n_f, inv_n) + P.eps);
+    const float var = div_n(row_sum<T>(q2.x + q2.y, red_s[group], flip, group, t), n_f, inv_n);
+    const float rstd = 1.0f / sqrtf(var + P.eps);
     if (t == 0 && P.mean != nullptr) P.mean[m] = mean, P.rstd[m] = rstd;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c0 = 8 * (k * T + t), cnt = count(k);
+      const int c0 = 8 * (k * threads + t), cnt = count(k);
       if (cnt == 0) continue;
       float g[8], b[8];
       if constexpr (!HOIST) params(k, g, b);
@@ -539,12 +657,12 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_long_kernel(const DropLnAr
     auto value = [&](int c0, int cnt, bool vec, float (&s)[8]) {
       float x[8];
       if (vec) widen8(x, load_raw8(P.x, m, c0, P.x.dt), P.x.dt);
-      else load_some8(x, P.x, m, c0, cnt);
+      else gather8(x, P.x, m, P.M, P.N, c0, cnt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] = 0.0f;
       if (P.r.p != nullptr) {
         if (vec) widen8(s, load_raw8(P.r, m, c0, P.r.dt), P.r.dt);
-        else load_some8(s, P.r, m, c0, cnt);
+        else gather8(s, P.r, m, P.M, P.N, c0, cnt);
       }
       if (P.d.on) {
         add_dropped8(s, x, draw8<true>((uint64_t)(m * groups + (c0 >> 2)), off, P.d), P.d);
@@ -578,8 +696,8 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_long_kernel(const DropLnAr
           store8(P.z, m, c0, cnt, vec, g, P.z.dt);
         }
       }
-      if (step == 0) mean = div_n(row_sum<1024>(acc, red, flip, 0), n_f, inv_n);
-      if (step == 1) rstd = 1.0f / sqrtf(div_n(row_sum<1024>(acc, red, flip, 0), n_f, inv_n) + P.eps);
+      if (step == 0) mean = div_n(row_sum<1024>(acc, red, flip, 0, threadIdx.x), n_f, inv_n);
+      if (step == 1) rstd = 1.0f / sqrtf(div_n(row_sum<1024>(acc, red, flip, 0, threadIdx.x), n_f, inv_n) + P.eps);
     }
     if (threadIdx.x == 0 && P.mean != nullptr) P.mean[m] = mean, P.rstd[m] = rstd;
   }
@@ -597,9 +715,9 @@ struct DropLnBwdArgs {
 };
 
 // With u = (s − μ)·rstd and g = dz·γ:  ds = rstd·(g − mean(g) − u·mean(g·u)) + ds_in,
-// dx = D(ds), dγ = Σ_m dz·u, dβ = Σ_m dz.  T threads share a row, two vectors each, staged rows
+// dx = D(ds), dγ = Σ_m dz·u, dβ = Σ_m dz.  T threads share a row, V vectors each, staged rows
 // ahead in shared memory; registers hold the row's g and u, γ, and the dγ, dβ sums of the thread's
-// columns over all its rows (1024 threads, which have half the registers, read the row from shared
+// columns over all its rows (512 threads, which have half the registers, read the row from shared
 // memory twice instead, for the sums and for the gradients).  A CTA of 256 (or T) threads holds R rows at a time; at the end its row groups' sums are
 // added in shared memory and stored as one partial row each of dγ and dβ, which
 // fl_ln_wgrad_kernel adds in a fixed order.
@@ -609,39 +727,47 @@ __host__ __device__ constexpr size_t ln_bwd_part_bytes(int t, int v) {
   return ln_bwd_block(t) > t ? (size_t)(ln_bwd_block(t) / t) * 16u * (size_t)v * (size_t)t * sizeof(float) : 0;
 }
 template <int T, int V, int XT, int ST, int ZT>
-__global__ void __launch_bounds__(ln_bwd_block(T), T <= 256 ? 2 : 1) fl_dropout_ln_bwd_kernel(const DropLnBwdArgs P) {
+__global__ void __launch_bounds__(ln_bwd_block(T), 1) fl_dropout_ln_bwd_kernel(const DropLnBwdArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   constexpr bool TYPED = XT >= 0;
   constexpr int BLOCK = ln_bwd_block(T);
   constexpr int R = BLOCK / T;
+  constexpr bool KEEP = T <= 256;  // the row's values and γ stay in registers
+  constexpr int VK = KEEP ? V : 1;
   extern __shared__ __align__(16) uint8_t ring_s[];
   __shared__ __align__(16) float2 red_s[R][2 * (T / 32)];
   const int xt = dt_of<XT>(P.dx), st = dt_of<ST>(P.s), zt = dt_of<ZT>(P.dz);
+  constexpr int threads = T, vectors = V * T;  // of a row
   const int group = threadIdx.x / T, t = threadIdx.x % T;
   int flip = 0;
   const DropOffset off = drop_offset(P.d);
   const long long groups = (P.N + 3) / 4;
   const float n_f = (float)P.N, inv_n = 1.0f / n_f;
   const long long m0 = (long long)blockIdx.x * R + group, step = (long long)gridDim.x * R;
+  const uint32_t zw = row_words(P.dz, vectors), sw = row_words(P.s, vectors), iw = row_words(P.ds_in, vectors);
+  const uint32_t slot_bytes = 16u * R * (zw + sw + iw);
   const uint32_t ring = smem_u32(ring_s);
-  const uint32_t zb = operand_bytes(P.dz, V, BLOCK), sb = operand_bytes(P.s, V, BLOCK);
-  const uint32_t slot_bytes = zb + sb + operand_bytes(P.ds_in, V, BLOCK);
+  const uint32_t zo = 16u * group * zw, so = 16u * (R * zw + group * sw), io = 16u * (R * (zw + sw) + group * iw);
   const bool has_in = P.ds_in.p != nullptr;
   auto count = [&](int k) {
-    const int left = P.N - 8 * (k * T + t);
+    const int left = P.N - 8 * (k * threads + t);
     return TYPED ? (left > 0 ? 8 : 0) : max(0, min(8, left));
   };
   auto prefetch = [&](long long m, uint32_t slot) {
-    if (m < P.M && (TYPED || P.vec)) {
+    if (m < P.M) {
+      if constexpr (TYPED) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c0 = 8 * (k * T + t);
-        if (count(k) == 8) {
-          stage_vec<V, BLOCK>(slot, P.dz, m, c0, k, zt);
-          stage_vec<V, BLOCK>(slot + zb, P.s, m, c0, k, st);
-          if (has_in) stage_vec<V, BLOCK>(slot + zb + sb, P.ds_in, m, c0, k, st);
+        for (int k = 0; k < V; ++k) {
+          if (count(k) == 0) continue;
+          stage_vec(slot + zo, P.dz, m, k * threads + t, vectors, zt);
+          stage_vec(slot + so, P.s, m, k * threads + t, vectors, st);
+          if (has_in) stage_vec(slot + io, P.ds_in, m, k * threads + t, vectors, st);
         }
+      } else {
+        stage_row(slot + zo, P.dz, m, P.M, P.N, t, threads);
+        stage_row(slot + so, P.s, m, P.M, P.N, t, threads);
+        if (has_in) stage_row(slot + io, P.ds_in, m, P.M, P.N, t, threads);
       }
     }
     cp_async_commit();
@@ -654,10 +780,8 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T <= 256 ? 2 : 1) fl_dropout_
     for (int i = 0; i < 8; ++i) pg[k][i] = pb[k][i] = 0.0f;
   auto param = [&](int k, float (&g)[8]) {
     const int cnt = count(k);
-    load_param8(g, P.gamma, P.param_dt, 8 * (k * T + t), cnt, TYPED || (P.vec && cnt == 8), 1.0f);
+    load_param8(g, P.gamma, P.param_dt, 8 * (k * threads + t), cnt, TYPED || (P.vec && cnt == 8), 1.0f);
   };
-  constexpr bool KEEP = T < 1024 || V == 1;  // the row's values and γ stay in registers
-  constexpr int VK = KEEP ? V : 1;
   float gam[VK][8];
   if constexpr (KEEP) {
 #pragma unroll
@@ -665,17 +789,21 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T <= 256 ? 2 : 1) fl_dropout_
       if (count(k) > 0) param(k, gam[k]);
   }
   int at = 0;
+  float next_mean = 0.0f, next_rstd = 0.0f;  // read a row ahead
+  if (m0 < P.M) next_mean = P.mean[m0], next_rstd = P.rstd[m0];
   for (long long m = m0; m < P.M; m += step) {
     const uint32_t slot = ring + at * slot_bytes;
-    const float mean = P.mean[m], rstd = P.rstd[m];
+    const float mean = next_mean, rstd = next_rstd;
+    if (m + step < P.M) next_mean = P.mean[m + step], next_rstd = P.rstd[m + step];
     // dz and u = (s − μ)·rstd of vector k (zeros past N)
     auto values = [&](int k, int cnt, float (&dz)[8], float (&u)[8]) {
-      if (TYPED || (P.vec && cnt == 8)) {
-        unstage_vec<V, BLOCK>(dz, slot, zt, k);
-        unstage_vec<V, BLOCK>(u, slot + zb, st, k);
+      const int vi = k * threads + t;
+      if constexpr (TYPED) {
+        unstage_vec(dz, slot + zo, vi, vectors, zt);
+        unstage_vec(u, slot + so, vi, vectors, st);
       } else {
-        load_some8(dz, P.dz, m, 8 * (k * T + t), cnt);
-        load_some8(u, P.s, m, 8 * (k * T + t), cnt);
+        unstage_row(dz, slot + zo, P.dz, m, vi, cnt);
+        unstage_row(u, slot + so, P.s, m, vi, cnt);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -685,6 +813,7 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T <= 256 ? 2 : 1) fl_dropout_
       }
     };
     wait_row(P.ahead);
+    if constexpr (!TYPED) row_barrier(group, threads);
     float2 a2 = make_float2(0.0f, 0.0f), b2 = a2;
     float g[VK][8], u[VK][8];
 #pragma unroll
@@ -699,18 +828,17 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T <= 256 ? 2 : 1) fl_dropout_
         const float2 z = pair_of(g[kk], j), w = pair_of(u[kk], j);
         put_pair(pg[k], j, fma2(z, w, pair_of(pg[k], j)));
         put_pair(pb[k], j, add2(z, pair_of(pb[k], j)));
-        // (past the row dz is 0; a γ read there is not: only dz·γ enters the sums)
         float2 q = mul2(z, pair_of(gam[kk], j));
         put_pair(g[kk], j, q);
         a2 = add2(a2, q);
         b2 = fma2(q, w, b2);
       }
     }
-    const float2 ab = row_sum2<T>(make_float2(a2.x + a2.y, b2.x + b2.y), red_s[group], flip, group);
+    const float2 ab = row_sum2<T>(make_float2(a2.x + a2.y, b2.x + b2.y), red_s[group], flip, group, t);
     const float ma = div_n(ab.x, n_f, inv_n), mb = div_n(ab.y, n_f, inv_n);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c0 = 8 * (k * T + t), cnt = count(k);
+      const int vi = k * threads + t, c0 = 8 * vi, cnt = count(k);
       if (cnt == 0) continue;
       const bool vec = TYPED || (P.vec && cnt == 8);
       const int kk = KEEP ? k : 0;
@@ -724,8 +852,8 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T <= 256 ? 2 : 1) fl_dropout_
 #pragma unroll
       for (int i = 0; i < 8; ++i) in[i] = 0.0f;
       if (has_in) {
-        if (vec) unstage_vec<V, BLOCK>(in, slot + zb + sb, st, k);
-        else load_some8(in, P.ds_in, m, c0, cnt);
+        if constexpr (TYPED) unstage_vec(in, slot + io, vi, vectors, st);
+        else unstage_row(in, slot + io, P.ds_in, m, vi, cnt);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -738,6 +866,7 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T <= 256 ? 2 : 1) fl_dropout_
         store8(P.dx, m, c0, cnt, vec, in, xt);
       }
     }
+    if constexpr (!TYPED) row_barrier(group, threads);  // every thread has read the slot
     prefetch(m + P.ahead * step, slot);
     at = at + 1 == P.ahead ? 0 : at + 1;
   }
@@ -772,7 +901,7 @@ __global__ void __launch_bounds__(ln_bwd_block(T), T <= 256 ? 2 : 1) fl_dropout_
   } else {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c0 = 8 * (k * T + t);
+      const int c0 = 8 * (k * threads + t);
       if (c0 >= P.N) continue;
       float4* q = reinterpret_cast<float4*>(out + c0);
       q[0] = make_float4(pg[k][0], pg[k][1], pg[k][2], pg[k][3]);
@@ -811,8 +940,8 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_bwd_long_kernel(const Drop
           widen8(dz, load_raw8(P.dz, m, c0, P.dz.dt), P.dz.dt);
           widen8(u, load_raw8(P.s, m, c0, P.s.dt), P.s.dt);
         } else {
-          load_some8(dz, P.dz, m, c0, cnt);
-          load_some8(u, P.s, m, c0, cnt);
+          gather8(dz, P.dz, m, P.M, P.N, c0, cnt);
+          gather8(u, P.s, m, P.M, P.N, c0, cnt);
         }
         load_param8(gam, P.gamma, P.param_dt, c0, cnt, vec, 1.0f);
 #pragma unroll
@@ -836,7 +965,7 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_bwd_long_kernel(const Drop
           if (P.ds_in.p != nullptr) {
             float in[8];
             if (vec) widen8(in, load_raw8(P.ds_in, m, c0, P.ds_in.dt), P.ds_in.dt);
-            else load_some8(in, P.ds_in, m, c0, cnt);
+            else gather8(in, P.ds_in, m, P.M, P.N, c0, cnt);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dz[i] += in[i];
           }
@@ -848,7 +977,7 @@ __global__ void __launch_bounds__(1024) fl_dropout_ln_bwd_long_kernel(const Drop
         }
       }
       if (step == 0) {
-        const float2 ab = row_sum2<1024>(make_float2(a, b), red, flip, 0);
+        const float2 ab = row_sum2<1024>(make_float2(a, b), red, flip, 0, threadIdx.x);
         ma = div_n(ab.x, n_f, inv_n);
         mb = div_n(ab.y, n_f, inv_n);
       }

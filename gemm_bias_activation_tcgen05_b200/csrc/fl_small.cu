@@ -9,9 +9,8 @@ using namespace fl::host;
 namespace {
 template <int DT>
 void (*by_rows(int64_t M))(SmallArgs) {
-  if (M <= 8) return fl_glu_small_kernel<GATE_SWIGLU, DT, 1, 1, SU1>;
-  if (M <= 16) return fl_glu_small_kernel<GATE_SWIGLU, DT, 2, 2, SU2>;
-  return fl_glu_small_kernel<GATE_SWIGLU, DT, 4, 2, SU2>;
+  if (M <= 8) return fl_glu_small_kernel<GATE_SWIGLU, DT, 1, 1, 8>;
+  return fl_glu_small_kernel<GATE_SWIGLU, DT, 2, 2, 2>;
 }
 }  // namespace
 
@@ -21,7 +20,7 @@ void fl::host::small_config(fl_plan_s* p) {
   p->small = true;
   p->pair = false;
   p->kernel = reinterpret_cast<const void*>(p->dtype == FL_BF16 ? by_rows<DT_BF16>(p->M) : by_rows<DT_F16>(p->M));
-  p->mma_n = (int)(p->M <= 8 ? 8 : p->M <= 16 ? 16 : 32);
+  p->mma_n = p->M <= 8 ? 8 : 16;
   p->out_tile_n = p->M <= 8 ? 8 : 16;
   p->split_k = 1;
   p->stages = 1;

@@ -1,35 +1,27 @@
-// fl_small.cuh — the gated linear unit of a few rows (serving: one new token of each of up to 32
+// fl_small.cuh — the gated linear unit of a few rows (serving: one new token of each of up to 16
 // sequences): h = act(x·Wgᵀ) ⊙ (x·Wuᵀ), bound by reading the weights once.
 //
-// A warp owns 8 output features: their 8 gate rows and 8 up rows of W are the 16 rows of an
+// Eight output features are a unit: their 8 gate rows and 8 up rows of W are the 16 rows of an
 // mma.sync.m16n8k16 operand A, the rows of x its B columns (8 at a time), so that gate and up of a
 // feature end in the same lane.  An inner product does not depend on the order of k, so the lanes
 // take k in an order of their own: in a step of 32 lane (g, t) holds k = 8t .. 8t + 7 of row g, one
 // 16-byte load, whose four words are the k pairs of two products, and the same k of x's row g.
 // Weights go from memory to the tensor core through registers: no shared memory, no barrier.
 // The products run far below the tensor core's rate (2·M operations a byte), so the legacy warp form
-// is enough, and it needs no staging.  The CTA's warps share the 8 features and take steps of k in
-// turn, four steps (256 bytes of each of 16 rows) at a time, all in flight; their sums meet in shared
-// memory in a fixed order.
+// is enough, and it needs no staging.  The CTA's warps share one unit and take steps of k in turn,
+// eight steps (512 bytes of each of 16 rows) at a time, all in flight; their sums meet in shared memory
+// in a fixed order.  From 9 rows on x's own loads count: a CTA then takes two units, two steps at a time.
+//
+// Measured with N 8192, K 4096 bf16 (134 MB of weights, 20.5 us at the copy rate): 1 row 21.2 us
+// (6.3 TB/s), 8 rows 23.0, 16 rows 26.6; 32 rows took 44.6, where the pair kernel takes 30.5, so it ends
+// at 16.  (1 row with four steps in flight 23-27 us, with four warps a CTA 22.9.)
 #pragma once
 #include "fl_pair.cuh"
 
 namespace fl {
 
-#ifndef SMR
-#define SMR 16
-#endif
-#ifndef SW
-#define SW 8
-#endif
-#ifndef SU1
-#define SU1 8
-#define SU2 2
-#define SC1 2
-#define SC2 1
-#endif
-constexpr int kSmallWarps = SW;
-constexpr int kSmallMaxRows = SMR;
+constexpr int kSmallWarps = 8;
+constexpr int kSmallMaxRows = 16;
 
 struct SmallArgs {
   const void *x, *w;
@@ -73,7 +65,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 
 // NT: blocks of 8 rows of x (M ≤ 8·NT); FT: blocks of 8 features a warp (and CTA) owns.
 template <int ACT, int DT, int NT, int FT, int U>
-__global__ void __launch_bounds__(kSmallWarps * 32, FT == 1 ? SC1 : SC2) fl_glu_small_kernel(const SmallArgs P) {
+__global__ void __launch_bounds__(kSmallWarps * 32, FT == 1 ? 2 : 1) fl_glu_small_kernel(const SmallArgs P) {
   constexpr int W = kSmallWarps;
   __shared__ float part[W][2][8 * FT][8 * NT + 1];  // [warp][gate, up][feature][row of x]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;

@@ -205,6 +205,26 @@ def test_dglu_options(fl):
     _dglu(fl, 70, 64, 0)  # dh = 0
 
 
+@pytest.mark.parametrize("kind", ["SWIGLU", "GEGLU_TANH"])
+def test_gates_at_the_ends_of_the_range(fl, kind):
+    """Gates as large as the type holds: the derivative is 1 or 0 there, never 0·∞."""
+    M, N, K = 64, 64, 64
+    dy, d_dy = mat(M, K, "bf16", 1, 0.5)
+    Wd, dW = mat(K, N, "bf16", 2)
+    gu = torch.randn(M, 2 * N, generator=torch.Generator().manual_seed(3)).bfloat16()
+    big = torch.tensor([250.0, -250.0, 1e19, -1e19, 3e38, -3e38, float("inf"), 0.0]).bfloat16()
+    gu[:, :N] = big.repeat(M, N // 8)
+    out = torch.empty(M, 2 * N, dtype=torch.bfloat16, device="cuda")
+    run(fl, fl.Plan(M, N, K, kind=KIND[kind][2], out_dtype="bf16", b_major=1), d_dy, dW, aux=gu.cuda(), out=out)
+    g, u = P.to64(gu[:, :N]), P.to64(gu[:, N:])
+    dh, d = dy @ Wd, acc_err(dy, Wd)
+    slope = np.where(g == 0, 0.5, (g > 0).astype(float))
+    within(P.to64(out[:, :N]), dh * u * slope, d * np.abs(u) + 3 * E * np.abs(dh * u), "bf16", "dg")
+    fin = np.abs(g) < 1e18  # the others overflow in the product with dh
+    within(np.where(fin, P.to64(out[:, N:]), 0), np.where(fin, dh * np.maximum(g, 0), 0), np.where(fin, d * np.abs(g), 0) + 1e-30,
+           "bf16", "du")
+
+
 def _wgrad(fl, M, N, tokens, dtype="bf16", out_dtype="f32", accumulate=False, scale=1.0, pad=0, in_place=False, res_dtype=None,
            noalloc=False):
     res_dtype = res_dtype or out_dtype

@@ -225,6 +225,20 @@ def test_dropout_layernorm_options(fl, kw):
     _forward(fl, 3, 16640, **kw)
 
 
+@pytest.mark.parametrize("N", [9, 65, 513, 1031, 2049, 4095, 5121, 8191, 8193, 16383])
+def test_rows_that_start_anywhere(fl, N):
+    """Odd widths, pitches and bases in every type: each row starts at another place of a 16-byte word."""
+    M = 37 if N < 4000 else 11
+    for types in (("bf16", "bf16", "bf16", "bf16"), ("f16", "f32", "f32", "f16"), ("f32", "bf16", "f16", "f32")):
+        for kw in (dict(), dict(off=1), dict(pad=3, off=5)):
+            _forward(fl, M, N, types, **kw)
+            _backward(fl, M, N, types, **kw)
+    _forward(fl, 400, N, pad=1)
+    _backward(fl, 400, N, pad=1)
+    _dropout(fl, M, N, "bf16", "bf16", 0.3, lds=(N + 3, N + 1, N), offs=(1, 0, 3))
+    _dropout(fl, M, N, "f32", "f16", 0.3, lds=(N + 3, N + 1, N + 2), offs=(1, 3, 5))
+
+
 def test_dropout_layernorm_in_place(fl):
     """z over x and sum over the residual: every element is read before it is written."""
     for M, N in [(500, 4096), (3, 20000)]:
