@@ -49,27 +49,41 @@ __host__ __device__ constexpr bool pair_a_mn(int epi) { return epi == EPI_GRAD; 
 __host__ __device__ constexpr bool pair_b_mn(int epi) { return epi == EPI_DGLU || epi == EPI_GRAD || epi == EPI_DGLU_PART; }
 __host__ __device__ constexpr bool pair_glu(int epi) { return epi == EPI_GLU || epi == EPI_GLU_AUX || epi == EPI_GLU_PART; }
 
-// σ(y) = 1/(1 + e^(-y)); e^(-y) and the reciprocal on the special-function unit (relative errors
-// near 2^-22), saturating to 0 and 1
-__device__ __forceinline__ float sigmoid_f(float y) { return rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * y)); }
-// The tanh GELU is x·σ(2c(x + 0.044715x³)), c = √(2/π), because (1 + tanh y)/2 = σ(2y): no
-// cancellation for negative x, so that both gates keep fp32 precision over their whole range.
-// act(x), and in `slope` act'(x) = σ + x·σ·(1 − σ)·y'(x).  In the second term x is held within ±200,
-// where 1 − σ or σ has long been 0: no 0·∞ for the largest values.
+// The gates are x·σ(y): y = x (SWIGLU), or y = 2c(x + 0.044715x³), c = √(2/π), for the tanh GELU,
+// because (1 + tanh w)/2 = σ(2w): no cancellation for negative x, so that both keep fp32 precision over
+// their whole range.  σ(y) = 1/(1 + e^(-y)) with e^(-y) and the reciprocal on the special-function unit
+// (relative errors near 2^-22), saturating to 0 and 1; e^(-y) is 2 to the power of x times a polynomial
+// in x² that holds the constants.  Two values at a time: eight epilogue warps are few for the arithmetic
+// of a tile, and the packed fp32 instructions halve it.
+// act(x), and in `slope` act'(x) = σ + x·σ·(1 − σ)·y'(x).  x is held within ±200 where only σ's ends
+// matter: no 0·∞ for the largest values.
+constexpr float kLog2E = 1.4426950408889634f, kTwoC = 2.0f * 0.79788456080286536f;
+template <int ACT>
+__device__ __forceinline__ float2 gate2(float2 x, float2& slope) {
+  const float2 one = make_float2(1.0f, 1.0f), minus = make_float2(-1.0f, -1.0f);
+  const float2 xc = make_float2(fminf(fmaxf(x.x, -200.0f), 200.0f), fminf(fmaxf(x.y, -200.0f), 200.0f));
+  float2 arg, dy = one;
+  if constexpr (ACT == GATE_SWIGLU) {
+    arg = mul2(xc, make_float2(-kLog2E, -kLog2E));
+  } else {
+    constexpr float c3 = -0.044715f * kTwoC * kLog2E, c1 = -kTwoC * kLog2E, d3 = 3.0f * 0.044715f * kTwoC;
+    const float2 x2 = mul2(xc, xc);
+    arg = mul2(xc, fma2(x2, make_float2(c3, c3), make_float2(c1, c1)));
+    dy = fma2(x2, make_float2(d3, d3), make_float2(kTwoC, kTwoC));
+  }
+  const float2 den = add2(make_float2(ex2_approx(arg.x), ex2_approx(arg.y)), one);
+  const float2 s = make_float2(rcp_approx(den.x), rcp_approx(den.y));
+  float2 w = mul2(xc, fma2(s, minus, one));
+  if constexpr (ACT != GATE_SWIGLU) w = mul2(w, dy);
+  slope = mul2(s, add2(w, one));
+  return mul2(x, s);
+}
 template <int ACT>
 __device__ __forceinline__ float gate_f(float x, float& slope) {
-  const float xc = fminf(fmaxf(x, -200.0f), 200.0f);
-  if constexpr (ACT == GATE_SWIGLU) {
-    const float s = sigmoid_f(x);
-    slope = s * fmaf(xc, 1.0f - s, 1.0f);
-    return x * s;
-  } else {
-    constexpr float k = 2.0f * 0.79788456080286536f;
-    const float x2 = xc * xc;
-    const float s = sigmoid_f(k * xc * fmaf(0.044715f, x2, 1.0f));
-    slope = s * fmaf(xc * (1.0f - s), k * fmaf(3.0f * 0.044715f, x2, 1.0f), 1.0f);
-    return x * s;
-  }
+  float2 sl;
+  const float2 a = gate2<ACT>(make_float2(x, x), sl);
+  slope = sl.x;
+  return a.x;
 }
 
 // Item i of a pair: its tile (and K split): units u = pair, pair + pairs, ... of tiles·splits,
@@ -425,11 +439,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 g = unpack2<OUT>(gw[e]), u = unpack2<OUT>(uw[e]);
-              const float h0 = __uint_as_float(ga[8 * c + 2 * e]), h1 = __uint_as_float(ga[8 * c + 2 * e + 1]);
-              float s0, s1;
-              const float a0 = gate_f<ACT>(g.x, s0), a1 = gate_f<ACT>(g.y, s1);
-              dg[e] = pack2<OUT>(h0 * u.x * s0, h1 * u.y * s1);
-              du[e] = pack2<OUT>(h0 * a0, h1 * a1);
+              const float2 dh = make_float2(__uint_as_float(ga[8 * c + 2 * e]), __uint_as_float(ga[8 * c + 2 * e + 1]));
+              float2 slope;
+              const float2 b2 = mul2(dh, gate2<ACT>(g, slope)), a2 = mul2(mul2(dh, u), slope);
+              dg[e] = pack2<OUT>(a2.x, a2.y);
+              du[e] = pack2<OUT>(b2.x, b2.y);
             }
             st_shared_u4(ag, dg[0], dg[1], dg[2], dg[3]);
             st_shared_u4(au, du[0], du[1], du[2], du[3]);
@@ -460,9 +474,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
           if constexpr (EPI == EPI_GLU || EPI == EPI_GLU_AUX) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float slope;
-              v[j] = gate_f<ACT>(__uint_as_float(ga[j]), slope) * __uint_as_float(gu[j]);
+            for (int j = 0; j < 32; j += 2) {
+              float2 slope;
+              const float2 g = make_float2(__uint_as_float(ga[j]), __uint_as_float(ga[j + 1]));
+              const float2 h = mul2(gate2<ACT>(g, slope), make_float2(__uint_as_float(gu[j]), __uint_as_float(gu[j + 1])));
+              v[j] = h.x;
+              v[j + 1] = h.y;
             }
           } else if constexpr (EPI != EPI_GLU_PART) {
 #pragma unroll
