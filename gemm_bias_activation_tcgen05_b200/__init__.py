@@ -252,7 +252,9 @@ def fl_layernorm(x, gamma, beta, z, M: int, N: int, x_dtype: str, z_dtype: str, 
 
 
 def _dropout(p: float, seed: int, offset: int, offset_dev):
-    """The dropout descriptor; seed and offset are taken modulo 2^64."""
+    """The dropout descriptor (None without dropout); seed and offset are taken modulo 2^64."""
+    if p == 0.0:
+        return None
     return ctypes.byref(fl_dropout_desc(float(p), 0, int(seed) % 2**64, int(offset) % 2**64, _ptr(offset_dev)))
 
 

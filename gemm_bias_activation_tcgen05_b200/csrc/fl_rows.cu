@@ -116,8 +116,11 @@ RowKernel<DropLnArgs> ln_kernel(int64_t N, RowTypes r) {
   if (N <= 512) return ln_of<32, 2>(r);
   if (N <= 1024) return ln_of<64, 2>(r);
   if (N <= 2048) return ln_of<128, 2>(r);
+  if (N <= 16 * 192) return ln_of<192, 2>(r);
   if (N <= 4096) return ln_of<256, 2>(r);
+  if (N <= 6144) return ln_of<384, 2>(r);
   if (N <= 8192) return ln_of<512, 2>(r);
+  if (N <= 12288) return ln_of<768, 2>(r);
   if (N <= 16384) return ln_of<1024, 2>(r);
   return {fl_dropout_ln_long_kernel, 0, 0, 1024};
 }
@@ -254,10 +257,11 @@ extern "C" fl_status fl_dropout_layernorm(const void* x, const void* residual, c
   const int64_t ctas = cdiv(M, k.threads == 0 ? 1 : k.block / k.threads);
   size_t smem = 0;
   if ((st = ring_of(k, slot_bytes(k, {&P.x, &P.r}), 0, &P, &smem))) return st;
-  int sms = 148, per_sm = 0;
+  int sms = 148, per_sm = 1;
   if ((st = num_sms(&sms))) return st;
   // one resident wave of CTAs that walk the rows: their rows ahead are then always in flight
-  FL_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, (const void*)k.fn, k.block, smem));
+  // (few rows need no query, which small calls would pay for)
+  if (ctas > sms) FL_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, (const void*)k.fn, k.block, smem));
   const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)std::max(1, per_sm) * sms);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   const cudaError_t err = launch_pdl_smem(k.fn, dim3(grid), (unsigned)k.block, smem, s, P);

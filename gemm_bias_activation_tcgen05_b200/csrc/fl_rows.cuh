@@ -489,11 +489,12 @@ struct DropLnArgs {
 // A CTA holds max(1, 128/T) rows at a time and walks the rows a grid apart; γ and β stay in registers (but for 1024 threads, which have 64 each).
 __host__ __device__ constexpr int ln_block(int t) { return t < 128 ? 128 : t; }
 template <int T, int V, int XT, int ST, int ZT>
-__global__ void __launch_bounds__(ln_block(T), T <= 128 ? 4 : 1) fl_dropout_ln_kernel(const DropLnArgs P) {
+__global__ void __launch_bounds__(ln_block(T), T <= 128 ? 4 : T == 192 ? 2 : 1) fl_dropout_ln_kernel(const DropLnArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   constexpr bool TYPED = XT >= 0, HOIST = T < 1024;
   constexpr int R = ln_block(T) / T;
+  static_assert(R <= 15, "a row group has a named barrier of its own, 1 to 15");
   extern __shared__ __align__(16) uint8_t ring_s[];
   __shared__ __align__(16) float2 red_s[R][2 * (T / 32)];
   const int xt = dt_of<XT>(P.x), st = ST >= 0 ? ST : (P.r.p != nullptr ? P.r.dt : P.s.dt), zt = dt_of<ZT>(P.z);
@@ -698,7 +699,7 @@ struct DropLnBwdArgs {
 // memory twice instead, for the sums and for the gradients).  A CTA of 256 (or T) threads holds R rows at a time; at the end its row groups' sums are
 // added in shared memory and stored as one partial row each of dγ and dβ, which
 // fl_ln_wgrad_kernel adds in a fixed order.
-__host__ __device__ constexpr int ln_bwd_block(int t) { return t < 256 ? 256 : t; }
+__host__ __device__ constexpr int ln_bwd_block(int t) { return 256 % t == 0 ? 256 : t; }
 // bytes of the row groups' column sums at the end
 __host__ __device__ constexpr size_t ln_bwd_part_bytes(int t, int v) {
   return ln_bwd_block(t) > t ? (size_t)(ln_bwd_block(t) / t) * 16u * (size_t)v * (size_t)t * sizeof(float) : 0;
@@ -710,6 +711,7 @@ __global__ void __launch_bounds__(ln_bwd_block(T), 1) fl_dropout_ln_bwd_kernel(c
   constexpr bool TYPED = XT >= 0;
   constexpr int BLOCK = ln_bwd_block(T);
   constexpr int R = BLOCK / T;
+  static_assert(R <= 15, "a row group has a named barrier of its own, 1 to 15");
   constexpr bool KEEP = T <= 256;  // the row's values and γ stay in registers
   constexpr int VK = KEEP ? V : 1;
   extern __shared__ __align__(16) uint8_t ring_s[];
