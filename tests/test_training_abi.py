@@ -148,5 +148,5 @@ def test_pair_configurations(fl, kind):
         assert st == fl.FL_OK, fl.fl_last_error()
         if i.cta_pair:
             assert i.smem_bytes <= 232448 and i.stages >= 3 and i.grid % 2 == 0 and 0 < i.grid <= 148
-            assert 1 <= i.split_k <= max(1, -(-K // 64)) and (kind == "WGRAD" or i.split_k == 1)
-        assert i.launches_per_execute == (2 if kind == "WGRAD" and i.split_k > 1 else 1)
+            assert 1 <= i.split_k <= max(1, -(-K // 64)) and (i.split_k == 1 or i.split_k * -(-M // 256) * -(-N // i.tile_n) <= 148)
+        assert i.launches_per_execute == (2 if i.split_k > 1 else 1)
