@@ -34,21 +34,20 @@ template <int EPI, int ACT>
 PairFn by_out(int out, int atoms) {
   return out == FL_BF16 ? by_atoms<EPI, ACT, DT_BF16>(atoms) : by_atoms<EPI, ACT, DT_F16>(atoms);
 }
-PairFn pair_kernel(int kind, int out, bool split, int atoms) {
-  const int epi = epi_of(kind);
-  if (split) {
-    return epi == EPI_GRAD   ? by_atoms<EPI_GRAD, GATE_SWIGLU, DT_F32>(atoms)
-           : epi == EPI_DGLU ? by_atoms<EPI_DGLU_PART, GATE_SWIGLU, DT_F32>(atoms)
-                             : by_atoms<EPI_GLU_PART, GATE_SWIGLU, DT_F32>(atoms);
-  }
-  switch (kind) {
-    case FL_EPI_SWIGLU: return by_out<EPI_GLU, GATE_SWIGLU>(out, atoms);
-    case FL_EPI_GEGLU_TANH_AUX: return by_out<EPI_GLU_AUX, GATE_GEGLU_TANH>(out, atoms);
-    case FL_EPI_SWIGLU_AUX: return by_out<EPI_GLU_AUX, GATE_SWIGLU>(out, atoms);
-    case FL_EPI_DGEGLU_TANH: return by_out<EPI_DGLU, GATE_GEGLU_TANH>(out, atoms);
-    case FL_EPI_DSWIGLU: return by_out<EPI_DGLU, GATE_SWIGLU>(out, atoms);
-    default:
-      return out == FL_F32 ? by_atoms<EPI_GRAD, GATE_SWIGLU, DT_F32>(atoms) : by_out<EPI_GRAD, GATE_SWIGLU>(out, atoms);
+template <int EPI>
+PairFn grad_kernel(int out, int atoms) {
+  return out == FL_F32 ? by_atoms<EPI, GATE_SWIGLU, DT_F32>(atoms) : by_out<EPI, GATE_SWIGLU>(out, atoms);
+}
+PairFn pair_kernel(int epi, bool geglu, int out, int atoms) {
+  switch (epi) {
+    case EPI_GLU: return by_out<EPI_GLU, GATE_SWIGLU>(out, atoms);  // (GEGLU_TANH has kernels of its own)
+    case EPI_GLU_AUX:
+      return geglu ? by_out<EPI_GLU_AUX, GATE_GEGLU_TANH>(out, atoms) : by_out<EPI_GLU_AUX, GATE_SWIGLU>(out, atoms);
+    case EPI_DGLU: return geglu ? by_out<EPI_DGLU, GATE_GEGLU_TANH>(out, atoms) : by_out<EPI_DGLU, GATE_SWIGLU>(out, atoms);
+    case EPI_GLU_PART: return by_atoms<EPI_GLU_PART, GATE_SWIGLU, DT_F32>(atoms);
+    case EPI_DGLU_PART: return by_atoms<EPI_DGLU_PART, GATE_SWIGLU, DT_F32>(atoms);
+    case EPI_GRAD_ADD: return grad_kernel<EPI_GRAD_ADD>(out, atoms);
+    default: return grad_kernel<EPI_GRAD>(out, atoms);
   }
 }
 void (*finish_kernel(int kind))(FinishArgs) {
@@ -60,11 +59,12 @@ void (*finish_kernel(int kind))(FinishArgs) {
       return is_geglu(kind) ? fl_split_finish_kernel<EPI_GLU, GATE_GEGLU_TANH> : fl_split_finish_kernel<EPI_GLU, GATE_SWIGLU>;
   }
 }
-// What the tile kernel itself computes and writes: with K splits, fp32 partial results.
+// What the tile kernel itself computes and writes: with K splits, fp32 partial results.  The residual
+// of a weight gradient comes and leaves in the same blocks when the types agree.
 int kernel_epi(const fl_plan_s* p) {
   const int epi = epi_of(p->epi.kind);
-  if (p->split_k == 1 || epi == EPI_GRAD) return epi;
-  return epi == EPI_DGLU ? EPI_DGLU_PART : EPI_GLU_PART;
+  if (p->split_k > 1) return epi == EPI_GRAD ? EPI_GRAD : epi == EPI_DGLU ? EPI_DGLU_PART : EPI_GLU_PART;
+  return epi == EPI_GRAD && p->epi.has_residual && p->epi.residual_dtype == p->epi.out_dtype ? EPI_GRAD_ADD : epi;
 }
 // Shared memory of the tile kernel: the ring, the epilogue warps' blocks, the barriers.
 struct PairLayout {
@@ -161,7 +161,10 @@ fl_status fl::host::pair_config(fl_plan_s* p, bool no_workspace) {
     const bool wide = p->mma_n == 256;
     p->k_atoms = (rounds == 1 || kb >= 20) && (double)rounds * kb * (wide ? 0.03 : 0.08) > (wide ? 2.6 : 1.4) ? 2 : 1;
   } else {
-    p->k_atoms = kb >= 8 ? 2 : 1;
+    // (an fp32 residual needs two 4 KB buffers a warp to come while another leaves: with one, 8192 x 2048
+    // of 1024 tokens 72 us against 48.5; 2048 x 2048 of 4096 tokens 30.8 against 31.3)
+    const bool wide_residual = kernel_epi(p) == EPI_GRAD_ADD && p->epi.out_dtype == FL_F32;
+    p->k_atoms = kb >= (wide_residual ? 48 : 8) ? 2 : 1;
   }
   p->num_kb = (int)cdiv(p->K, p->k_atoms * kPairBk);
   p->stages = 0;
@@ -170,7 +173,8 @@ fl_status fl::host::pair_config(fl_plan_s* p, bool no_workspace) {
   if (p->stages < 2) return fail(FL_ERR_UNSUPPORTED, "fl_plan: shared memory too small");
   p->smem = (int)pair_layout(p).total;
   p->grid = (int)(2 * std::min<int64_t>((int64_t)p->tiles_a * p->tiles_b * p->split_k, P));
-  p->kernel = reinterpret_cast<const void*>(pair_kernel(p->epi.kind, p->epi.out_dtype, p->split_k > 1, p->k_atoms));
+  p->kernel = reinterpret_cast<const void*>(
+      pair_kernel(kernel_epi(p), is_geglu(p->epi.kind), p->split_k > 1 ? FL_F32 : p->epi.out_dtype, p->k_atoms));
   p->launches = p->split_k > 1 ? 2 : 1;
   return FL_OK;
 }
@@ -267,6 +271,7 @@ fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, voi
     // whole 16-byte granules of a row go out by TMA, the ragged remainder by plain stores
     k.n_tma = (int)(N * eo / 16 * 16 / eo);
     st = tile(&m0, out, e.out_dtype, (uint64_t)std::max<int64_t>(k.n_tma, 16 / (int64_t)eo), M, (uint64_t)e.ldo * eo);
+    if (!st && epi == EPI_GRAD_ADD) st = tile(&m1, residual, e.out_dtype, N, M, (uint64_t)e.ldr * eo);
     if (!st && epi == EPI_GLU_AUX) {
       char* g = static_cast<char*>(aux);
       if (!(st = tile(&m1, g, e.out_dtype, N, M, 2 * N * eo))) st = tile(&m2, g + N * eo, e.out_dtype, N, M, 2 * N * eo);

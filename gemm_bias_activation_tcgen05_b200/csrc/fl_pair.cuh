@@ -21,10 +21,10 @@
 //
 // Stages are ATOMS x 64 deep in K.  Each hand-over of a stage costs the tensor pipe some 40 clocks, so
 // 128-deep stages (64 KB a CTA, three of them) run long K loops faster: weight gradient 8192 x 4096 of
-// 4096 tokens 202.6 -> 185.6 us (1.48 PFLOP/s), SwiGLU backward 4096 x 8192 x 4096 224.7 -> 216.1.  They leave 4 KB of
-// shared memory for each epilogue warp; 64-deep ones (five or six) leave 8 KB, and with them the
-// epilogue, which bounds short K loops, waits less for its blocks: SwiGLU backward
-// 2048 x 2048 of 256 deep 13.5 us with 128-deep stages, 11.5 with 64-deep ones.
+// 4096 tokens 202.6 -> 185.6 us (1.48 PFLOP/s), SwiGLU backward 4096 x 8192 x 4096 224.7 -> 216.1.  They
+// leave 4 KB of shared memory for each epilogue warp; 64-deep ones (five or six) leave 8 KB, and with them
+// the epilogue, which bounds short K loops, waits less for its blocks: SwiGLU backward 2048 x 2048 of 256
+// deep 13.5 us with 128-deep stages, 11.5 with 64-deep ones.
 //
 // Every wait is bounded; on expiry the kernel records an error code and unwinds.
 #pragma once
@@ -32,7 +32,9 @@
 
 namespace fl {
 
-enum PairEpi : int { EPI_GLU = 0, EPI_GLU_AUX = 1, EPI_DGLU = 2, EPI_GRAD = 3, EPI_GLU_PART = 4, EPI_DGLU_PART = 5 };
+enum PairEpi : int {
+  EPI_GLU = 0, EPI_GLU_AUX = 1, EPI_DGLU = 2, EPI_GRAD = 3, EPI_GLU_PART = 4, EPI_DGLU_PART = 5, EPI_GRAD_ADD = 6
+};
 enum GateAct : int { GATE_SWIGLU = 0, GATE_GEGLU_TANH = 1 };
 
 constexpr int kPairThreads = (kEpiWarp0 + 8) * 32;
@@ -45,8 +47,8 @@ constexpr uint32_t kPairBarBytes = 8u * (uint32_t)kPairBars;
 // bytes of one 32 x 32 block of a type, and of the blocks of one epilogue warp
 __host__ __device__ constexpr uint32_t pair_block_bytes(int out) { return out == DT_F32 ? 4096u : 2048u; }
 __host__ __device__ constexpr uint32_t pair_warp_staging(int atoms) { return atoms == 1 ? 8192u : 4096u; }
-__host__ __device__ constexpr bool pair_a_mn(int epi) { return epi == EPI_GRAD; }
-__host__ __device__ constexpr bool pair_b_mn(int epi) { return epi == EPI_DGLU || epi == EPI_GRAD || epi == EPI_DGLU_PART; }
+__host__ __device__ constexpr bool pair_a_mn(int epi) { return epi == EPI_GRAD || epi == EPI_GRAD_ADD; }
+__host__ __device__ constexpr bool pair_b_mn(int epi) { return pair_a_mn(epi) || epi == EPI_DGLU || epi == EPI_DGLU_PART; }
 __host__ __device__ constexpr bool pair_glu(int epi) { return epi == EPI_GLU || epi == EPI_GLU_AUX || epi == EPI_GLU_PART; }
 
 // The gates are x·σ(y): y = x (SWIGLU), or y = 2c(x + 0.044715x³), c = √(2/π), for the tanh GELU,
@@ -144,6 +146,24 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   if constexpr (DT == DT_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   else return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
+// v += this lane's 32 values of a block
+template <int OUT>
+__device__ __forceinline__ void add_block(float (&v)[32], uint32_t base, int lane) {
+#pragma unroll
+  for (int c = 0; c < (OUT == DT_F32 ? 8 : 4); ++c) {
+    const uint4 x = ld_shared_u4(OUT == DT_F32 ? blk32_addr(base, lane, c) : blk16_addr(base, lane, c));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (OUT == DT_F32) {
+        v[4 * c + e] += __uint_as_float(w[e]);
+      } else {
+        const float2 f = unpack2<OUT>(w[e]);
+        v[8 * c + 2 * e] += f.x, v[8 * c + 2 * e + 1] += f.y;
+      }
+    }
+  }
+}
 // 32 elements of a row of type dt from column n0 by plain (coherent) loads, since the output may be
 // the same buffer; zeros past N
 __device__ __forceinline__ void load_res32(float (&r)[32], const void* base, long long row_off, int n0, int N, int dt) {
@@ -184,7 +204,8 @@ __device__ __forceinline__ void load_res32(float (&r)[32], const void* base, lon
 
 // Tensor maps: tmA, tmB operands (GLU: tmB gate rows, tmB2 up rows).  tm0..tm3 the epilogue's:
 //   GLU      tm0 h            GLU_AUX  tm0 h, tm1 g, tm2 u
-//   DGLU     tm0 g, tm1 u (loads), tm2 dg, tm3 du        GRAD, *_PART  tm0 y (or the workspace)
+//   DGLU     tm0 g, tm1 u (loads), tm2 dg, tm3 du        GRAD, *_PART  tm0 y (or the workspace),
+//            GRAD_ADD as GRAD, tm1 the residual
 // p.M is the number of output rows, p.N its columns; columns from p.n_tma on (a ragged end below 16
 // bytes) are stored one by one.  In a workspace p.N is the padded width of one partial result (of g,
 // which u follows, for GLU_PART), and p.split_rows ≥ p.M the rows of one split, a multiple of 32.
@@ -208,31 +229,30 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   auto tempty_bar = [&](int b) { return bars + 8u * (2 * NS + 2 + b); };
   const uint32_t drain_bar = bars + 8u * (2 * NS + 4);
   const uint32_t tmem_slot = bars + 8u * (2 * NS + 5);
-  auto aux_bar = [&](int w, int b) { return bars + 8u * (2 * NS + 6 + 2 * w + b); };  // DGLU: g, u of a block
+  // arrival of what a block of an epilogue warp works on: DGLU g and u, GRAD_ADD the residual
+  auto aux_bar = [&](int w, int b) { return bars + 8u * (2 * NS + 6 + 2 * w + b); };
 
   const uint32_t rank = cluster_ctarank();
   const int cluster_id = blockIdx.x >> 1;
   const int num_clusters = gridDim.x >> 1;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
+  if (warp == 0) {
+    const int nbars = 2 * NS + 6 + (EPI == EPI_DGLU || EPI == EPI_GRAD_ADD ? 16 : 0);
+    for (int i = lane; i < nbars; i += 32) {
+      const int j = i - 2 * NS;
+      // (j = 5 is the place of the TMEM address; both CTAs' epilogue warps arrive on the two before the drain's)
+      if (j != 5) mbar_init(bars + 8u * i, j == 2 || j == 3 ? 16 : 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), 16);  // the epilogue warps of both CTAs
-    }
-    mbar_init(drain_bar, 1);
-    if constexpr (EPI == EPI_DGLU)
-      for (int i = 0; i < 16; ++i) mbar_init(aux_bar(i >> 1, i & 1), 1);
     fence_mbarrier_init();
-    if (p.num_kb > 0) {  // with K = 0 the operand maps are left unencoded and never used
-      prefetch_tensormap(&tmA);
-      prefetch_tensormap(&tmB);
-      if (GLU) prefetch_tensormap(&tmB2);
+    if (lane == 0) {
+      if (p.num_kb > 0) {  // with K = 0 the operand maps are left unencoded and never used
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+        if (GLU) prefetch_tensormap(&tmB2);
+      }
+      prefetch_tensormap(&tm0);
     }
-    prefetch_tensormap(&tm0);
+    __syncwarp();
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, p.tmem_cols);
@@ -372,17 +392,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     bool ok = true;
     PairItem itm;
     // DGLU: g, u tiles arrive in, and dg, du leave from, GU pairs of buffers in turn; lane 0 sends for
-    // those of block b of an item into pair `to`
-    constexpr uint32_t GU = pair_warp_staging(ATOMS) / 4096u;
+    // those of block b of an item into pair `to`.  GRAD_ADD, the form of GRAD for a residual of the output's
+    // type: the same, GU buffers.  (Read by the lanes, a row each, which is 32 lines an
+    // instruction, the residual took longer than the products: 8191 x 1999 fp32 of 777 tokens 47.7 us, 33.5 so;
+    // 768 x 768 of 256 8.6 and 6.8.)
+    constexpr bool IN_PLACE = EPI == EPI_DGLU || EPI == EPI_GRAD_ADD;
+    constexpr uint32_t GU_BYTES = EPI == EPI_GRAD_ADD ? pair_block_bytes(OUT) : 4096u;
+    constexpr uint32_t GU = pair_warp_staging(ATOMS) / GU_BYTES < 2u ? 1u : 2u;
     auto fetch_gu = [&](const PairItem& w, int b, uint32_t to) {
       const int n0 = w.tb * p.out_tile_n + c_begin + 32 * b, r0 = w.ta * 256 + (int)rank * 128 + q * 32;
-      mbar_arrive_expect_tx(aux_bar(ew, (int)to), 4096u);
-      tma_load_2d(stg + to * 4096u, &tm0, aux_bar(ew, (int)to), n0, r0);
-      tma_load_2d(stg + to * 4096u + 2048u, &tm1, aux_bar(ew, (int)to), n0, r0);
+      mbar_arrive_expect_tx(aux_bar(ew, (int)to), GU_BYTES);
+      if constexpr (EPI == EPI_DGLU) {
+        tma_load_2d(stg + to * 4096u, &tm0, aux_bar(ew, (int)to), n0, r0);
+        tma_load_2d(stg + to * 4096u + 2048u, &tm1, aux_bar(ew, (int)to), n0, r0);
+      } else {
+        tma_load_2d(stg + to * GU_BYTES, &tm1, aux_bar(ew, (int)to), n0, r0);
+      }
     };
-    uint32_t fetched = 0;  // DGLU: blocks whose tiles have been sent for
+    uint32_t fetched = 0;  // blocks whose tiles have been sent for
     bool more = pair_item(p, cluster_id, num_clusters, 0, itm);
-    if constexpr (EPI == EPI_DGLU) {
+    if constexpr (IN_PLACE) {
       if (more) {
         if (lane == 0) fetch_gu(itm, 0, 0);
         fetched = 1;  // (the others follow, GU − 1 blocks ahead of their use)
@@ -412,21 +441,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) ga[j] = gu[j] = 0u;
         }
+        const bool last = b + 1 == nblk;
+        auto fetch_next = [&]() {
+          // (the other buffer's stores, or this one's, have read it)
+          if (!last || have_next) {
+            if (lane == 0) {
+              bulk_wait_group_read<0>();
+              if (last) fetch_gu(nxt, 0, (blk + 1) % GU);
+              else fetch_gu(itm, b + 1, (blk + 1) % GU);
+            }
+            ++fetched;
+          }
+        };
         if constexpr (EPI == EPI_DGLU) {
           const uint32_t slot = blk % GU;
           const uint32_t sg = stg + slot * 4096u, su = sg + 2048u;
-          const bool last = b + 1 == nblk;
-          auto fetch_next = [&]() {
-            // (the other pair's stores, or this one's, have read it)
-            if (!last || have_next) {
-              if (lane == 0) {
-                bulk_wait_group_read<0>();
-                if (last) fetch_gu(nxt, 0, (blk + 1) % GU);
-                else fetch_gu(itm, b + 1, (blk + 1) % GU);
-              }
-              ++fetched;
-            }
-          };
           if constexpr (GU > 1) fetch_next();
           if (acc_any) tmem_wait_ld();
           if (!warp_wait_bounded(aux_bar(ew, (int)slot), (blk / GU) & 1u, p, lane)) { ok = false; break; }
@@ -484,7 +513,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           } else if constexpr (EPI != EPI_GLU_PART) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ga[j]);
-            if (p.residual != nullptr && m_ok && n0 < p.N) {
+            if constexpr (EPI == EPI_GRAD_ADD) {
+              const uint32_t slot = blk % GU;
+              if constexpr (GU > 1) fetch_next();
+              if (!warp_wait_bounded(aux_bar(ew, (int)slot), (blk / GU) & 1u, p, lane)) { ok = false; break; }
+              add_block<OUT>(v, stg + slot * GU_BYTES, lane);
+            }
+            if (EPI == EPI_GRAD && p.residual != nullptr && m_ok && n0 < p.N) {
               float r[32];
               load_res32(r, p.residual, (long long)m * p.ldr, n0, p.N, p.res_dtype);
 #pragma unroll
@@ -496,13 +531,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
           }
           if constexpr (EPI != EPI_GLU_PART) {
-            if ((EPI == EPI_GLU || EPI == EPI_GRAD) && n0 + 32 > p.n_tma && n0 < p.N && m_ok) {
+            if ((EPI == EPI_GLU || pair_a_mn(EPI)) && n0 + 32 > p.n_tma && n0 < p.N && m_ok) {
               // ragged row end: a TMA store writes whole 16-byte granules
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 if (n0 + j >= p.n_tma && n0 + j < p.N) store_elem<OUT>(p.out, (long long)m * p.ldo + n0 + j, v[j]);
             }
-            emit(&tm0, n0, row, inside, v);
+            if constexpr (EPI == EPI_GRAD_ADD) {
+              const uint32_t at = stg + (blk % GU) * GU_BYTES;
+              put_block<OUT>(at, lane, v);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (inside) tma_store_2d(&tm0, at, n0, row);
+                bulk_commit_group();
+              }
+              if constexpr (GU == 1) fetch_next();
+            } else {
+              emit(&tm0, n0, row, inside, v);
+            }
           }
         }
         if (b + 1 == nblk) {
@@ -520,7 +567,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       itm = nxt;
       more = have_next;
     }
-    if constexpr (EPI == EPI_DGLU) {
+    if constexpr (IN_PLACE) {
       // after a wait that gave up: no tile may still be on its way when the CTA leaves
       for (uint32_t f = blk; f < fetched; ++f) (void)warp_wait_bounded(aux_bar(ew, (int)(f % GU)), (f / GU) & 1u, p, lane);
     }

@@ -272,6 +272,15 @@ def test_weight_grad_options(fl):
     assert _wgrad(fl, 256, 256, 16384)["split_k"] > 1
 
 
+@pytest.mark.parametrize("out_dtype,tokens,deep", [("f32", 130, 1), ("f32", 3100, 2), ("bf16", 300, 1), ("bf16", 700, 2), ("f16", 64, 1)])
+def test_weight_grad_of_many_tiles_accumulates(fl, out_dtype, tokens, deep):
+    """Several tiles a pair: the residual of a tile's first block is sent for during the tile before; both stage depths."""
+    for M, N, in_place in [(2600, 2600, False), (5001, 1339, True)]:
+        info = _wgrad(fl, M, N, tokens, dtype="f16" if out_dtype == "f16" else "bf16", out_dtype=out_dtype, accumulate=True,
+                      in_place=in_place)
+        assert info["split_k"] == 1 and info["stages"] == (5 if deep == 1 else 3) and info["grid"] == 148
+
+
 def test_plans_repeat_bit_for_bit_and_in_graphs(fl):
     """Each kind twice on new data through one plan, eagerly and in a replayed graph: the same bits."""
     M, N, K = 520, 776, 264
