@@ -111,12 +111,23 @@ RowKernel<DropLnBwdArgs> ln_bwd_of(RowTypes r) {
   }
 }
 
-// Forward: two vectors a thread.
-RowKernel<DropLnArgs> ln_kernel(int64_t N, RowTypes r) {
+// Threads and vectors of a row.  Threads beyond the row's end load and store nothing, but they draw (to
+// skip that in the forward pass cost full rows 1.5 %), issue the row's sums and hold its barriers, so a
+// row wants to fill its threads: two vectors a thread, or three where the row then needs half the threads
+// that two would take (768: 32 of them, 96 vectors, no barrier).  A row of three vectors takes longer,
+// which shows where an SM walks few of them.
+// Three against two, in us (bf16): forward 32768 x 768 40.7 and 50.0, 16384 x 1280 39.2 and 47.4,
+// 8192 x 768 13.1 and 14.5, but 2048 x 768 7.0 and 6.2; backward 32768 x 768 48.3 and 64.9, 16384 x 1280
+// 51.7 and 65.6, 8192 x 2560 54.8 and 60.3, 4096 x 5120 47.6 and 50.3, 2048 x 768 10.6 and 10.8, but
+// 64 x 768 5.3 and 4.8.
+RowKernel<DropLnArgs> ln_kernel(int64_t M, int64_t N, int sms, RowTypes r) {
+  const bool many = M > 24 * (int64_t)sms;
   if (N <= 512) return ln_of<32, 2>(r);
+  if (N <= 768 && many) return ln_of<32, 3>(r);
   if (N <= 1024) return ln_of<64, 2>(r);
+  if (N <= 1536 && many) return ln_of<64, 3>(r);
   if (N <= 2048) return ln_of<128, 2>(r);
-  if (N <= 16 * 192) return ln_of<192, 2>(r);
+  if (N <= 16 * 192) return many ? ln_of<128, 3>(r) : ln_of<192, 2>(r);
   if (N <= 4096) return ln_of<256, 2>(r);
   if (N <= 6144) return ln_of<384, 2>(r);
   if (N <= 8192) return ln_of<512, 2>(r);
@@ -124,14 +135,19 @@ RowKernel<DropLnArgs> ln_kernel(int64_t N, RowTypes r) {
   if (N <= 16384) return ln_of<1024, 2>(r);
   return {fl_dropout_ln_long_kernel, 0, 0, 1024};
 }
-// Backward: two vectors a thread (what a row costs beside its elements is spread over both), four
-// where a CTA of 256 threads then still holds the row.
-RowKernel<DropLnBwdArgs> ln_bwd_kernel(int64_t N, RowTypes r) {
+// Backward: four vectors where a CTA of 256 threads then still holds the row.
+RowKernel<DropLnBwdArgs> ln_bwd_kernel(int64_t M, int64_t N, int sms, RowTypes r) {
+  const bool many = M > 4 * (int64_t)sms;
   if (N <= 512) return ln_bwd_of<32, 2>(r);
+  if (N <= 768 && many) return ln_bwd_of<32, 3>(r);
   if (N <= 1024) return ln_bwd_of<64, 2>(r);
+  if (N <= 1536 && many) return ln_bwd_of<64, 3>(r);
   if (N <= 2048) return ln_bwd_of<128, 2>(r);
+  if (N <= 16 * 192 && many) return ln_bwd_of<128, 3>(r);
   if (N <= 4096) return ln_bwd_of<256, 2>(r);
+  if (N <= 6144) return ln_bwd_of<256, 3>(r);
   if (N <= 8192) return ln_bwd_of<256, 4>(r);
+  if (N <= 12288) return ln_bwd_of<512, 3>(r);
   if (N <= 16384) return ln_bwd_of<512, 4>(r);
   return {fl_dropout_ln_bwd_long_kernel, 0, 0, 1024};
 }
@@ -148,11 +164,13 @@ struct BwdGeom {
 };
 BwdGeom bwd_geom(int64_t M, int64_t N, int sms, RowTypes r) {
   BwdGeom g;
-  g.k = ln_bwd_kernel(N, r);
+  g.k = ln_bwd_kernel(M, N, sms, r);
   const int64_t ctas = cdiv(M, g.k.threads == 0 ? 1 : g.k.block / g.k.threads);
   g.grid = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)sms));
   g.ws_ld = (int)(cdiv(N, 8) * 8);
-  g.bytes = (size_t)g.grid * 2 * (size_t)g.ws_ld * sizeof(float);
+  // (a partial row for each row or SM, whichever are fewer: no less than the grid, and never less for more
+  // rows, so that a workspace for the longest batch serves the shorter ones)
+  g.bytes = (size_t)std::max<int64_t>(1, std::min<int64_t>(M, (int64_t)sms)) * 2 * (size_t)g.ws_ld * sizeof(float);
   return g;
 }
 
@@ -164,11 +182,11 @@ size_t slot_bytes(const RowKernel<Args>& k, std::initializer_list<const Mat*> op
   for (const Mat* m : ops) words += row_words(*m, k.vecs * k.threads);
   return 16 * words * (size_t)(k.block / k.threads);
 }
-// The ring: two slots of `slot` bytes, or one where two do not fit (but at least `least` bytes).  A ring that takes a CTA above 48 KB with the kernel's own arrays
-// needs the kernel's opt-in.
+// The ring: two slots of `slot` bytes, or one where two do not fit (but at least `least` bytes).  A ring
+// that takes a CTA above 48 KB with the kernel's own arrays needs the kernel's opt-in.
 template <typename Args>
 fl_status ring_of(const RowKernel<Args>& k, size_t slot, size_t least, Args* P, size_t* smem) {
-  constexpr size_t kMost = 200 * 1024;  // of the 227 KB of a CTA; the kernels' own arrays take at most 17 KB
+  constexpr size_t kMost = 200 * 1024;  // of the 227 KB of a CTA; the kernels' own arrays take little
   P->ahead = kRowsAhead * slot <= kMost ? kRowsAhead : 1;
   *smem = std::max(P->ahead * slot, least);
   if (*smem > 24 * 1024)
@@ -253,12 +271,12 @@ extern "C" fl_status fl_dropout_layernorm(const void* x, const void* residual, c
   P.N = (int)N;
   P.param_dt = param_dtype;
   P.eps = eps;
-  const RowKernel<DropLnArgs> k = ln_kernel(N, row_types(P.vec, M, N, x_dtype, sum_dtype, z_dtype));
+  int sms = 148, per_sm = 1;
+  if ((st = num_sms(&sms))) return st;
+  const RowKernel<DropLnArgs> k = ln_kernel(M, N, sms, row_types(P.vec, M, N, x_dtype, sum_dtype, z_dtype));
   const int64_t ctas = cdiv(M, k.threads == 0 ? 1 : k.block / k.threads);
   size_t smem = 0;
   if ((st = ring_of(k, slot_bytes(k, {&P.x, &P.r}), 0, &P, &smem))) return st;
-  int sms = 148, per_sm = 1;
-  if ((st = num_sms(&sms))) return st;
   // one resident wave of CTAs that walk the rows: their rows ahead are then always in flight
   // (few rows need no query, which small calls would pay for)
   if (ctas > sms) FL_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, (const void*)k.fn, k.block, smem));
@@ -330,9 +348,8 @@ extern "C" fl_status fl_dropout_layernorm_backward(
   P.ws_ld = g.ws_ld;
   P.param_dt = param_dtype;
   size_t smem = 0;
-  if ((st = ring_of(g.k, slot_bytes(g.k, {&P.dz, &P.s, &P.ds_in}),
-                    g.k.block == g.k.threads || g.k.threads == 0 || !P.ws ? 0 : ln_bwd_part_bytes(g.k.threads, g.k.vecs), &P, &smem)))
-    return st;
+  const size_t parts = g.k.threads > 0 && P.ws ? ln_bwd_part_bytes(g.k.threads, g.k.vecs) : 0;
+  if ((st = ring_of(g.k, slot_bytes(g.k, {&P.dz, &P.s, &P.ds_in}), parts, &P, &smem))) return st;
   cudaError_t err = launch_pdl_smem(g.k.fn, dim3((unsigned)g.grid), (unsigned)g.k.block, smem, s, P);
   if (err != cudaSuccess) return fail(FL_ERR_CUDA, "%s: kernel launch: %s", who, cudaGetErrorString(err));
   if (params) {

@@ -149,7 +149,10 @@ __device__ __forceinline__ void widen8(float (&v)[8], const Raw8& r, int dt) {
   } else if (dt == DT_BF16) {
     // (a byte permutation, not a shift, which would go to the multiplications' pipe)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(__byte_perm(w[i], 0u, 0x1044)), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(__byte_perm(w[i], 0u, 0x1044));
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -486,10 +489,13 @@ struct DropLnArgs {
 
 // T threads hold a row, V vectors of eight each (N ≤ 8·V·T): the row is read once, stays in
 // registers through the mean, Σ(s − μ)² and the normalisation, and every output is written once.
-// A CTA holds max(1, 128/T) rows at a time and walks the rows a grid apart; γ and β stay in registers (but for 1024 threads, which have 64 each).
+// A CTA holds max(1, 128/T) rows at a time and walks the rows a grid apart; γ and β stay in registers
+// (but for 1024 threads, which have 64 each).  Three vectors need 150 to 168 registers: three CTAs of 128
+// threads an SM (with four, 128 registers spilled: 16384 x 1536 with an fp32 stream 66.6 us against 50.2).
 __host__ __device__ constexpr int ln_block(int t) { return t < 128 ? 128 : t; }
 template <int T, int V, int XT, int ST, int ZT>
-__global__ void __launch_bounds__(ln_block(T), T <= 128 ? 4 : T == 192 ? 2 : 1) fl_dropout_ln_kernel(const DropLnArgs P) {
+__global__ void __launch_bounds__(ln_block(T), V == 3 ? 3 : T <= 128 ? 4 : T == 192 ? 2 : 1)
+    fl_dropout_ln_kernel(const DropLnArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   constexpr bool TYPED = XT >= 0, HOIST = T < 1024;
@@ -696,9 +702,9 @@ struct DropLnBwdArgs {
 // dx = D(ds), dγ = Σ_m dz·u, dβ = Σ_m dz.  T threads share a row, V vectors each, staged rows
 // ahead in shared memory; registers hold the row's g and u, γ, and the dγ, dβ sums of the thread's
 // columns over all its rows (512 threads, which have half the registers, read the row from shared
-// memory twice instead, for the sums and for the gradients).  A CTA of 256 (or T) threads holds R rows at a time; at the end its row groups' sums are
-// added in shared memory and stored as one partial row each of dγ and dβ, which
-// fl_ln_wgrad_kernel adds in a fixed order.
+// memory twice instead, for the sums and for the gradients).  A CTA of 256 (or T) threads holds R rows at
+// a time; at the end its row groups' sums are added in shared memory and stored as one partial row each
+// of dγ and dβ, which fl_ln_wgrad_kernel adds in a fixed order.
 __host__ __device__ constexpr int ln_bwd_block(int t) { return 256 % t == 0 ? 256 : t; }
 // bytes of the row groups' column sums at the end
 __host__ __device__ constexpr size_t ln_bwd_part_bytes(int t, int v) {

@@ -302,7 +302,7 @@ fl_status fl_dropout_layernorm(const void* x, const void* residual, const void* 
  *   be null (not wanted), not all.  dres and dx may each be dz's, dsum's or sum's own buffer with
  *   the same type and pitch (not both the same one).  M = 0 gives dgamma = dbeta = 0.
  *   workspace: needed for dgamma and dbeta; fl_layernorm_grad_workspace_size bytes (for the
- *   current device), 16-byte aligned, owned by the caller, no initial contents needed.  Calls
+ *   current device; never less for more rows), 16-byte aligned, owned by the caller, no initial contents needed.  Calls
  *   that overlap on the GPU must not share it.
  * Errors: FL_ERR_INVALID_ARG (null operand, no output, size, ld < N, dtype, p, workspace),
  * FL_ERR_ALIGNMENT, FL_ERR_CUDA. */

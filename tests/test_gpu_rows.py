@@ -341,6 +341,20 @@ def test_dropout_layernorm_backward_types(fl, types):
         _backward(fl, M, N, types)
 
 
+@pytest.mark.parametrize("M,N", [(3600, 520), (3601, 768), (3600, 767), (3600, 1032), (3600, 1535), (3600, 2056), (3600, 2305)])
+@pytest.mark.parametrize("types", [("bf16", "bf16", "bf16", "bf16"), ("f16", "f32", "f16", "f32"), ("f32", "f32", "f32", "bf16")])
+def test_many_rows_of_three_vectors_a_thread(fl, M, N, types):
+    """Enough rows for the kernels that hold three vectors a thread; widths that leave threads idle, odd ones too."""
+    _forward(fl, M, N, types)
+    _backward(fl, M, N, types)
+
+
+@pytest.mark.parametrize("M,N", [(40, 4104), (300, 6144), (21, 5003), (9, 8200), (160, 12288), (5, 10001)])
+def test_wide_rows_of_three_vectors_a_thread_backward(fl, M, N):
+    _backward(fl, M, N)
+    _backward(fl, M, N, ("f32", "f32", "f32", "f32"), stream_grad=False)
+
+
 @pytest.mark.parametrize("kw", [dict(affine=False), dict(p=0.0), dict(p=0.75), dict(want="dx"), dict(want="dres"),
                                 dict(want="dgamma"), dict(want="dbeta"), dict(want="dres dgamma dbeta"), dict(pad=3),
                                 dict(pad=8), dict(off=1), dict(seed=2**64 - 1, offset=2**64 - 1)])
@@ -361,6 +375,12 @@ def test_backward_in_place(fl):
         torch.cuda.synchronize()
         check_backward(dict(dres=P.to64(b), dx=P.to64(a)), P.to64(dz), P.to64(dsum), s64, mean.astype(np.float64),
                        rstd.astype(np.float64), None, 0.3, 9, 0, ("bf16",) * 3, f"in place {M}x{N}")
+
+
+def test_a_workspace_for_many_rows_serves_fewer(fl):
+    for N in (768, 1000, 1536, 2560, 4096, 8200, 20000):
+        sizes = [fl.fl_layernorm_grad_workspace_size(M, N) for M in (0, 1, 7, 100, 147, 148, 149, 591, 592, 593, 3552, 3553, 100000)]
+        assert sizes == sorted(sizes) and all(n % 16 == 0 for n in sizes)
 
 
 def test_backward_of_no_rows_and_repeatable(fl):
