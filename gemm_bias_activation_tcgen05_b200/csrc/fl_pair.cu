@@ -47,6 +47,8 @@ PairFn pair_kernel(int epi, bool geglu, int out, int atoms) {
     case EPI_GLU_PART: return by_atoms<EPI_GLU_PART, GATE_SWIGLU, DT_F32>(atoms);
     case EPI_DGLU_PART: return by_atoms<EPI_DGLU_PART, GATE_SWIGLU, DT_F32>(atoms);
     case EPI_GRAD_ADD: return grad_kernel<EPI_GRAD_ADD>(out, atoms);
+    case EPI_RUNS: return &fl_pair_tcgen05<EPI_RUNS, GATE_SWIGLU, DT_F32, 2>;
+    case EPI_RUNS_ADD: return &fl_pair_tcgen05<EPI_RUNS_ADD, GATE_SWIGLU, DT_F32, 2>;
     default: return grad_kernel<EPI_GRAD>(out, atoms);
   }
 }
@@ -60,11 +62,15 @@ void (*finish_kernel(int kind))(FinishArgs) {
   }
 }
 // What the tile kernel itself computes and writes: with K splits, fp32 partial results.  The residual
-// of a weight gradient comes and leaves in the same blocks when the types agree.
+// of a weight gradient comes and leaves by TMA when the types agree.  Long fp32 sums are taken in runs.
 int kernel_epi(const fl_plan_s* p) {
   const int epi = epi_of(p->epi.kind);
-  if (p->split_k > 1) return epi == EPI_GRAD ? EPI_GRAD : epi == EPI_DGLU ? EPI_DGLU_PART : EPI_GLU_PART;
-  return epi == EPI_GRAD && p->epi.has_residual && p->epi.residual_dtype == p->epi.out_dtype ? EPI_GRAD_ADD : epi;
+  const bool split = p->split_k > 1;
+  if (epi == EPI_DGLU) return split ? EPI_DGLU_PART : epi;
+  if (epi != EPI_GRAD) return split ? EPI_GLU_PART : epi;
+  const bool runs = (split || p->epi.out_dtype == FL_F32) && cdiv(cdiv(p->K, kPairBk), p->split_k) * kPairBk > kPairRun;
+  const bool add = !split && p->epi.has_residual && p->epi.residual_dtype == p->epi.out_dtype;
+  return runs ? (add ? EPI_RUNS_ADD : EPI_RUNS) : add ? EPI_GRAD_ADD : EPI_GRAD;
 }
 // Shared memory of the tile kernel: the ring, the epilogue warps' blocks, the barriers.
 struct PairLayout {
@@ -161,10 +167,9 @@ fl_status fl::host::pair_config(fl_plan_s* p, bool no_workspace) {
     const bool wide = p->mma_n == 256;
     p->k_atoms = (rounds == 1 || kb >= 20) && (double)rounds * kb * (wide ? 0.03 : 0.08) > (wide ? 2.6 : 1.4) ? 2 : 1;
   } else {
-    // (an fp32 residual needs two 4 KB buffers a warp to come while another leaves: with one, 8192 x 2048
-    // of 1024 tokens 72 us against 48.5; 2048 x 2048 of 4096 tokens 30.8 against 31.3)
-    const bool wide_residual = kernel_epi(p) == EPI_GRAD_ADD && p->epi.out_dtype == FL_F32;
-    p->k_atoms = kb >= (wide_residual ? 48 : 8) ? 2 : 1;
+    // (an fp32 residual in short sums needs two 4 KB buffers a warp to come while another leaves: 8192 x 2048
+    // of 1024 tokens in one sum 48.5 us so, 72 with one)
+    p->k_atoms = kb >= 8 && !(kernel_epi(p) == EPI_GRAD_ADD && p->epi.out_dtype == FL_F32) ? 2 : 1;
   }
   p->num_kb = (int)cdiv(p->K, p->k_atoms * kPairBk);
   p->stages = 0;
@@ -271,7 +276,7 @@ fl_status fl::host::pair_execute(fl_plan_s* p, const void* A, const void* W, voi
     // whole 16-byte granules of a row go out by TMA, the ragged remainder by plain stores
     k.n_tma = (int)(N * eo / 16 * 16 / eo);
     st = tile(&m0, out, e.out_dtype, (uint64_t)std::max<int64_t>(k.n_tma, 16 / (int64_t)eo), M, (uint64_t)e.ldo * eo);
-    if (!st && epi == EPI_GRAD_ADD) st = tile(&m1, residual, e.out_dtype, N, M, (uint64_t)e.ldr * eo);
+    if (!st && (epi == EPI_GRAD_ADD || epi == EPI_RUNS_ADD)) st = tile(&m1, residual, e.out_dtype, N, M, (uint64_t)e.ldr * eo);
     if (!st && epi == EPI_GLU_AUX) {
       char* g = static_cast<char*>(aux);
       if (!(st = tile(&m1, g, e.out_dtype, N, M, 2 * N * eo))) st = tile(&m2, g + N * eo, e.out_dtype, N, M, 2 * N * eo);

@@ -33,7 +33,8 @@
 namespace fl {
 
 enum PairEpi : int {
-  EPI_GLU = 0, EPI_GLU_AUX = 1, EPI_DGLU = 2, EPI_GRAD = 3, EPI_GLU_PART = 4, EPI_DGLU_PART = 5, EPI_GRAD_ADD = 6
+  EPI_GLU = 0, EPI_GLU_AUX = 1, EPI_DGLU = 2, EPI_GRAD = 3, EPI_GLU_PART = 4, EPI_DGLU_PART = 5,
+  EPI_GRAD_ADD = 6, EPI_RUNS = 7, EPI_RUNS_ADD = 8
 };
 enum GateAct : int { GATE_SWIGLU = 0, GATE_GEGLU_TANH = 1 };
 
@@ -47,9 +48,18 @@ constexpr uint32_t kPairBarBytes = 8u * (uint32_t)kPairBars;
 // bytes of one 32 x 32 block of a type, and of the blocks of one epilogue warp
 __host__ __device__ constexpr uint32_t pair_block_bytes(int out) { return out == DT_F32 ? 4096u : 2048u; }
 __host__ __device__ constexpr uint32_t pair_warp_staging(int atoms) { return atoms == 1 ? 8192u : 4096u; }
-__host__ __device__ constexpr bool pair_a_mn(int epi) { return epi == EPI_GRAD || epi == EPI_GRAD_ADD; }
+__host__ __device__ constexpr bool pair_a_mn(int epi) {
+  return epi == EPI_GRAD || epi == EPI_GRAD_ADD || epi == EPI_RUNS || epi == EPI_RUNS_ADD;
+}
 __host__ __device__ constexpr bool pair_b_mn(int epi) { return pair_a_mn(epi) || epi == EPI_DGLU || epi == EPI_DGLU_PART; }
 __host__ __device__ constexpr bool pair_glu(int epi) { return epi == EPI_GLU || epi == EPI_GLU_AUX || epi == EPI_GLU_PART; }
+
+// The tensor core's accumulators round towards zero, which costs an fp32 result 1e-9 of its norm for each
+// k of a sum: 4.4e-6 at 4096 tokens, 1.9e-5 at 16384.  So fp32 sums of more than 896 tokens (EPI_RUNS) are
+// taken in runs of 896, each in an accumulator of its own, which the epilogue warps add in registers,
+// rounded to nearest (half of the tile's columns a warp: 128 registers), while the next run is multiplied:
+// 9e-7 whatever the tokens.  A run costs 0.4 us a tile: 2048 x 2048 of 4096 tokens 25.6 -> 28 us.
+constexpr int kPairRun = 896;
 
 // The gates are x·σ(y): y = x (SWIGLU), or y = 2c(x + 0.044715x³), c = √(2/π), for the tanh GELU,
 // because (1 + tanh w)/2 = σ(2w): no cancellation for negative x, so that both keep fp32 precision over
@@ -164,48 +174,44 @@ __device__ __forceinline__ void add_block(float (&v)[32], uint32_t base, int lan
     }
   }
 }
-// 32 elements of a row of type dt from column n0 by plain (coherent) loads, since the output may be
-// the same buffer; zeros past N
-__device__ __forceinline__ void load_res32(float (&r)[32], const void* base, long long row_off, int n0, int N, int dt) {
-  if (n0 + 32 <= N) {
-    if (dt == DT_F32) {
-      const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + row_off + n0);
+__device__ __forceinline__ float load_dt(const void* p, long long i, int dt) {
+  if (dt == DT_F32) return reinterpret_cast<const float*>(p)[i];
+  if (dt == DT_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(reinterpret_cast<const __half*>(p)[i]);
+}
+// v += 32 elements of a row of type dt from column n0 (none past N), by plain (coherent) loads, since the
+// output may be the same buffer
+__device__ __forceinline__ void add_res32(float (&v)[32], const void* base, long long row_off, int n0, int N, int dt) {
+  if (n0 + 32 <= N && dt == DT_F32) {
+    const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + row_off + n0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 f = q[i];
-        r[4 * i] = f.x, r[4 * i + 1] = f.y, r[4 * i + 2] = f.z, r[4 * i + 3] = f.w;
-      }
-    } else {
-      const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + row_off + n0);
+    for (int i = 0; i < 8; ++i) {
+      const float4 f = q[i];
+      v[4 * i] += f.x, v[4 * i + 1] += f.y, v[4 * i + 2] += f.z, v[4 * i + 3] += f.w;
+    }
+  } else if (n0 + 32 <= N) {
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + row_off + n0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = q[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < 4; ++i) {
+      const uint4 x = q[i];
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = dt == DT_BF16 ? unpack2<DT_BF16>(w[e]) : unpack2<DT_F16>(w[e]);
-          r[8 * i + 2 * e] = f.x, r[8 * i + 2 * e + 1] = f.y;
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = dt == DT_BF16 ? unpack2<DT_BF16>(w[e]) : unpack2<DT_F16>(w[e]);
+        v[8 * i + 2 * e] += f.x, v[8 * i + 2 * e + 1] += f.y;
       }
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      r[j] = 0.0f;
-      if (n0 + j < N) {
-        const long long i = row_off + n0 + j;
-        if (dt == DT_F32) r[j] = reinterpret_cast<const float*>(base)[i];
-        else if (dt == DT_BF16) r[j] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[i]);
-        else r[j] = __half2float(reinterpret_cast<const __half*>(base)[i]);
-      }
-    }
+    for (int j = 0; j < 32; ++j)
+      if (n0 + j < N) v[j] += load_dt(base, row_off + n0 + j, dt);
   }
 }
 
 // Tensor maps: tmA, tmB operands (GLU: tmB gate rows, tmB2 up rows).  tm0..tm3 the epilogue's:
 //   GLU      tm0 h            GLU_AUX  tm0 h, tm1 g, tm2 u
 //   DGLU     tm0 g, tm1 u (loads), tm2 dg, tm3 du        GRAD, *_PART  tm0 y (or the workspace),
-//            GRAD_ADD as GRAD, tm1 the residual
+//            RUNS as GRAD; GRAD_ADD, RUNS_ADD as GRAD, tm1 the residual
 // p.M is the number of output rows, p.N its columns; columns from p.n_tma on (a ragged end below 16
 // bytes) are stored one by one.  In a workspace p.N is the padded width of one partial result (of g,
 // which u follows, for GLU_PART), and p.split_rows ≥ p.M the rows of one split, a multiple of 32.
@@ -217,6 +223,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const __grid_constant__ CUtensorMap tm3, const __grid_constant__ KParams p) {
   constexpr bool GLU = pair_glu(EPI);
   constexpr bool A_MN = pair_a_mn(EPI), B_MN = pair_b_mn(EPI);
+  constexpr bool SUMS = EPI == EPI_RUNS || EPI == EPI_RUNS_ADD;
+  constexpr int RUN = kPairRun / (ATOMS * kPairBk);  // stages of a run
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5;
@@ -229,7 +237,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   auto tempty_bar = [&](int b) { return bars + 8u * (2 * NS + 2 + b); };
   const uint32_t drain_bar = bars + 8u * (2 * NS + 4);
   const uint32_t tmem_slot = bars + 8u * (2 * NS + 5);
-  // arrival of what a block of an epilogue warp works on: DGLU g and u, GRAD_ADD the residual
+  // arrival of what a block of an epilogue warp works on: DGLU g and u, GRAD_ADD and RUNS_ADD the residual
   auto aux_bar = [&](int w, int b) { return bars + 8u * (2 * NS + 6 + 2 * w + b); };
 
   const uint32_t rank = cluster_ctarank();
@@ -237,7 +245,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int num_clusters = gridDim.x >> 1;
 
   if (warp == 0) {
-    const int nbars = 2 * NS + 6 + (EPI == EPI_DGLU || EPI == EPI_GRAD_ADD ? 16 : 0);
+    const int nbars = 2 * NS + 6 + (EPI == EPI_DGLU || EPI == EPI_GRAD_ADD || EPI == EPI_RUNS_ADD ? 16 : 0);
     for (int i = lane; i < nbars; i += 32) {
       const int j = i - 2 * NS;
       // (j = 5 is the place of the TMEM address; both CTAs' epilogue warps arrive on the two before the drain's)
@@ -327,34 +335,39 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         bo[k] = B_MN ? k * 128u : (k >> 2) * (p.b_atom_bytes >> 4) + (k & 3) * 2u;
       }
       const uint32_t idesc = p.idesc;
-      uint32_t local = 0;
+      uint32_t n = 0;  // accumulators handed over
       StageRing rs;
       bool ok = true, issued = false;
       PairItem itm;
-      for (; ok && pair_item(p, cluster_id, num_clusters, (int)local, itm); ++local) {
-        const uint32_t buf = local & 1u;
-        if (!wait_bounded(tempty_bar(buf), ((local >> 1) & 1u) ^ 1u, p, true)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + buf * (uint32_t)p.mma_n;
-        for (int kb = itm.kb0; kb < itm.kb1; ++kb, rs.next((uint32_t)NS)) {
-          const int s = (int)rs.s;
-          if (!wait_bounded(full_bar(s), rs.ph, p)) { ok = false; break; }
+      for (int ii = 0; ok && pair_item(p, cluster_id, num_clusters, ii, itm); ++ii) {
+        int kb = itm.kb0;
+        do {
+          const int first = kb, end = SUMS ? min(itm.kb1, kb + RUN) : itm.kb1;
+          const uint32_t buf = n & 1u;
+          if (!wait_bounded(tempty_bar(buf), ((n >> 1) & 1u) ^ 1u, p, true)) { ok = false; break; }
           tc_fence_after();
-          const uint64_t da = da0 + (uint64_t)s * stage_step;
-          const uint64_t db = db0 + (uint64_t)s * stage_step;
+          const uint32_t d_tmem = tmem_base + buf * (uint32_t)p.mma_n;
+          for (; kb < end; ++kb, rs.next((uint32_t)NS)) {
+            const int s = (int)rs.s;
+            if (!wait_bounded(full_bar(s), rs.ph, p)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t da = da0 + (uint64_t)s * stage_step;
+            const uint64_t db = db0 + (uint64_t)s * stage_step;
 #pragma unroll
-          for (int k = 0; k < STEPS; ++k)
-            umma_f16_pair(d_tmem, da + ao[k], db + bo[k], idesc, (kb > itm.kb0 || k > 0) ? 1u : 0u);
-          umma_commit_pair_both(empty_bar(s));
-          issued = true;
-        }
-        if (!ok) break;
-        if (itm.kb1 > itm.kb0) {
-          umma_commit_pair_both(tfull_bar(buf));
-        } else {
-          mbar_arrive(tfull_bar(buf));
-          mbar_arrive_remote(mapa_shared(tfull_bar(buf), 1));
-        }
+            for (int k = 0; k < STEPS; ++k)
+              umma_f16_pair(d_tmem, da + ao[k], db + bo[k], idesc, (kb > first || k > 0) ? 1u : 0u);
+            umma_commit_pair_both(empty_bar(s));
+            issued = true;
+          }
+          if (!ok) break;
+          if (end > first) {
+            umma_commit_pair_both(tfull_bar(buf));
+          } else {
+            mbar_arrive(tfull_bar(buf));
+            mbar_arrive_remote(mapa_shared(tfull_bar(buf), 1));
+          }
+          ++n;
+        } while (kb < itm.kb1);
       }
       if (issued) {  // no MMA may still be running when TMEM is released
         umma_commit_pair(drain_bar);
@@ -375,11 +388,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // next one has read it, then fills and stores it.
     constexpr int SLOTS = (int)(pair_warp_staging(ATOMS) / pair_block_bytes(OUT));
     uint32_t slot_at = 0;
-    auto emit = [&](const CUtensorMap* map, int x, int y, bool inside, const float (&v)[32]) {
+    auto emit = [&](const CUtensorMap* map, int x, int y, bool inside, int own, const float (&v)[32]) {
       if (lane == 0) bulk_wait_group_read<SLOTS - 1>();
       __syncwarp();
       const uint32_t at = stg + slot_at * pair_block_bytes(OUT);
-      put_block<OUT>(at, lane, v);
+      put_block<OUT>(at, own, v);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -387,6 +400,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         bulk_commit_group();
       }
       slot_at = slot_at + 1 == (uint32_t)SLOTS ? 0u : slot_at + 1;
+    };
+    // ragged row end: a TMA store writes whole 16-byte granules
+    auto store_ragged = [&](int n0, int m, bool m_ok, const float (&v)[32]) {
+      if (n0 + 32 > p.n_tma && n0 < p.N && m_ok) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (n0 + j >= p.n_tma && n0 + j < p.N) store_elem<OUT>(p.out, (long long)m * p.ldo + n0 + j, v[j]);
+      }
     };
     uint32_t blk = 0;  // blocks this warp has begun (DGLU: the g, u tiles alternate between two buffers)
     bool ok = true;
@@ -396,8 +417,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // type: the same, GU buffers.  (Read by the lanes, a row each, which is 32 lines an
     // instruction, the residual took longer than the products: 8191 x 1999 fp32 of 777 tokens 47.7 us, 33.5 so;
     // 768 x 768 of 256 8.6 and 6.8.)
-    constexpr bool IN_PLACE = EPI == EPI_DGLU || EPI == EPI_GRAD_ADD;
-    constexpr uint32_t GU_BYTES = EPI == EPI_GRAD_ADD ? pair_block_bytes(OUT) : 4096u;
+    // RUNS_ADD takes the whole tile's residual into its sums at the tile's start, during the first run.
+    constexpr bool IN_PLACE = EPI == EPI_DGLU || EPI == EPI_GRAD_ADD || EPI == EPI_RUNS_ADD;
+    constexpr uint32_t GU_BYTES = EPI == EPI_GRAD_ADD || EPI == EPI_RUNS_ADD ? pair_block_bytes(OUT) : 4096u;
     constexpr uint32_t GU = pair_warp_staging(ATOMS) / GU_BYTES < 2u ? 1u : 2u;
     auto fetch_gu = [&](const PairItem& w, int b, uint32_t to) {
       const int n0 = w.tb * p.out_tile_n + c_begin + 32 * b, r0 = w.ta * 256 + (int)rank * 128 + q * 32;
@@ -417,20 +439,131 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         fetched = 1;  // (the others follow, GU − 1 blocks ahead of their use)
       }
     }
+    uint32_t n = 0;  // accumulators taken over
+    // this warp's TMEM reads of an accumulator are done: hand its share back to the leader
+    auto hand_back = [&](uint32_t buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank != 0) mbar_arrive_remote(mapa_shared(tempty_bar(buf), 0));
+        else mbar_arrive(tempty_bar(buf));
+      }
+    };
     while (more) {
       PairItem nxt;
-      const bool have_next = pair_item(p, cluster_id, num_clusters, (int)local + 1, nxt);
-      const uint32_t buf = local & 1u;
+      bool have_next = false;
+      if constexpr (!SUMS) have_next = pair_item(p, cluster_id, num_clusters, (int)local + 1, nxt);
       const bool acc_any = itm.kb1 > itm.kb0;
       const int row0 = itm.ta * 256 + (int)rank * 128 + q * 32;
       const int m = row0 + lane;
       const bool m_ok = m < p.M;
       const int n_tile0 = itm.tb * p.out_tile_n;
-      if (!warp_wait_bounded(tfull_bar(buf), (local >> 1) & 1u, p, lane, true)) { ok = false; break; }
+      // block b + 1 of the item, or the next item's first, once the other buffer's stores, or this one's,
+      // have read it
+      auto fetch_next = [&](int b) {
+        const bool last = b + 1 == nblk;
+        if (!last || have_next) {
+          if (lane == 0) {
+            bulk_wait_group_read<0>();
+            if (last) fetch_gu(nxt, 0, (blk + 1) % GU);
+            else fetch_gu(itm, b + 1, (blk + 1) % GU);
+          }
+          ++fetched;
+        }
+      };
+      // block b of a result y = (v + residual)·scale; false: a wait gave up
+      auto grad_block = [&](int b, float (&v)[32]) {
+        const int n0 = n_tile0 + c_begin + 32 * b;
+        const bool inside = n0 < p.n_tma && (p.split_rows == 0 || row0 < p.split_rows);
+        const int row = itm.split * p.split_rows + row0;
+        const uint32_t at = stg + (blk % GU) * GU_BYTES;
+        int own = lane;  // (hidden from the compiler, which would keep the blocks' addresses in registers)
+        if constexpr (SUMS) asm volatile("" : "+r"(own));
+        if constexpr (EPI == EPI_GRAD_ADD) {
+          if constexpr (GU > 1) fetch_next(b);
+          if (!warp_wait_bounded(aux_bar(ew, (int)(blk % GU)), (blk / GU) & 1u, p, lane)) return false;
+          add_block<OUT>(v, at, own);
+        }
+        if ((EPI == EPI_GRAD || EPI == EPI_RUNS) && p.residual != nullptr && m_ok && n0 < p.N)
+          add_res32(v, p.residual, (long long)m * p.ldr, n0, p.N, p.res_dtype);
+        if (p.scale != 1.0f) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= p.scale;
+        }
+        store_ragged(n0, m, m_ok, v);
+        if constexpr (EPI == EPI_GRAD_ADD) {
+          put_block<OUT>(at, own, v);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (inside) tma_store_2d(&tm0, at, n0, row);
+            bulk_commit_group();
+          }
+          if constexpr (GU == 1) fetch_next(b);
+        } else {
+          emit(&tm0, n0, row, inside, own, v);
+        }
+        if constexpr (!SUMS) ++blk;
+        return true;
+      };
+      if constexpr (SUMS) {
+        float sum[4][32];  // (a tile has two or four blocks a warp)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[b][j] = 0.0f;
+        if constexpr (EPI == EPI_RUNS_ADD) {
+          static_assert(GU == 1, "one buffer: a block is fetched when the one before it has been read");
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            if (b >= nblk) break;
+            if (!warp_wait_bounded(aux_bar(ew, 0), blk & 1u, p, lane)) { ok = false; break; }
+            add_block<OUT>(sum[b], stg, lane);
+            __syncwarp();
+            ++blk;
+            if (b + 1 < nblk) fetch_next(b);
+          }
+          if (!ok) break;
+        }
+        int kb = itm.kb0;
+        do {
+          const uint32_t buf = n & 1u;
+          if (!warp_wait_bounded(tfull_bar(buf), (n >> 1) & 1u, p, lane, true)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + buf * (uint32_t)p.mma_n + (uint32_t)c_begin;
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            if (b >= 2 * nblk || !acc_any) break;
+            uint32_t g[16];
+            tmem_ld16(tacc + 16u * b, g);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[b >> 1][16 * (b & 1) + j] += __uint_as_float(g[j]);
+          }
+          hand_back(buf);
+          ++n;
+          kb += RUN;
+        } while (kb < itm.kb1);
+        if (!ok) break;
+        have_next = pair_item(p, cluster_id, num_clusters, (int)local + 1, nxt);  // (now, for want of registers)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (b >= nblk) break;
+          if (!grad_block(b, sum[b])) { ok = false; break; }
+        }
+        if (!ok) break;
+        if constexpr (EPI == EPI_RUNS_ADD) fetch_next(nblk - 1);
+        ++local;
+        itm = nxt;
+        more = have_next;
+        continue;
+      }
+      const uint32_t buf = n & 1u;
+      if (!warp_wait_bounded(tfull_bar(buf), (n >> 1) & 1u, p, lane, true)) { ok = false; break; }
       tc_fence_after();
       const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + buf * (uint32_t)p.mma_n;
 #pragma unroll 1
-      for (int b = 0; b < nblk; ++b, ++blk) {
+      for (int b = 0; b < nblk; ++b) {
         const int cb = c_begin + 32 * b;
         const int n0 = n_tile0 + cb;
         uint32_t ga[32], gu[32];
@@ -441,22 +574,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) ga[j] = gu[j] = 0u;
         }
-        const bool last = b + 1 == nblk;
-        auto fetch_next = [&]() {
-          // (the other buffer's stores, or this one's, have read it)
-          if (!last || have_next) {
-            if (lane == 0) {
-              bulk_wait_group_read<0>();
-              if (last) fetch_gu(nxt, 0, (blk + 1) % GU);
-              else fetch_gu(itm, b + 1, (blk + 1) % GU);
-            }
-            ++fetched;
-          }
-        };
         if constexpr (EPI == EPI_DGLU) {
           const uint32_t slot = blk % GU;
           const uint32_t sg = stg + slot * 4096u, su = sg + 2048u;
-          if constexpr (GU > 1) fetch_next();
+          if constexpr (GU > 1) fetch_next(b);
           if (acc_any) tmem_wait_ld();
           if (!warp_wait_bounded(aux_bar(ew, (int)slot), (blk / GU) & 1u, p, lane)) { ok = false; break; }
 #pragma unroll
@@ -486,83 +607,45 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             bulk_commit_group();
           }
-          if constexpr (GU == 1) fetch_next();
+          if constexpr (GU == 1) fetch_next(b);
+          ++blk;
         } else {
           if (acc_any) tmem_wait_ld();
-          const bool inside = n0 < p.n_tma && (p.split_rows == 0 || row0 < p.split_rows);
-          const int row = itm.split * p.split_rows + row0;
           float v[32];
-          if constexpr (EPI == EPI_GLU_AUX || EPI == EPI_GLU_PART) {
+          if constexpr (pair_a_mn(EPI) || EPI == EPI_DGLU_PART) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ga[j]);
-            emit(EPI == EPI_GLU_AUX ? &tm1 : &tm0, n0, row, inside, v);
+            if (!grad_block(b, v)) { ok = false; break; }
+          } else {
+            const bool inside = n0 < p.n_tma && (p.split_rows == 0 || row0 < p.split_rows);
+            const int row = itm.split * p.split_rows + row0;
+            if constexpr (EPI == EPI_GLU_AUX || EPI == EPI_GLU_PART) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(gu[j]);
-            if constexpr (EPI == EPI_GLU_AUX) emit(&tm2, n0, row, inside, v);
-            else emit(&tm0, p.N + n0, row, inside, v);
-          }
-          if constexpr (EPI == EPI_GLU || EPI == EPI_GLU_AUX) {
+              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ga[j]);
+              emit(EPI == EPI_GLU_AUX ? &tm1 : &tm0, n0, row, inside, lane, v);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              float2 slope;
-              const float2 g = make_float2(__uint_as_float(ga[j]), __uint_as_float(ga[j + 1]));
-              const float2 h = mul2(gate2<ACT>(g, slope), make_float2(__uint_as_float(gu[j]), __uint_as_float(gu[j + 1])));
-              v[j] = h.x;
-              v[j + 1] = h.y;
+              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(gu[j]);
+              if constexpr (EPI == EPI_GLU_AUX) emit(&tm2, n0, row, inside, lane, v);
+              else emit(&tm0, p.N + n0, row, inside, lane, v);
             }
-          } else if constexpr (EPI != EPI_GLU_PART) {
+            if constexpr (EPI == EPI_GLU || EPI == EPI_GLU_AUX) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ga[j]);
-            if constexpr (EPI == EPI_GRAD_ADD) {
-              const uint32_t slot = blk % GU;
-              if constexpr (GU > 1) fetch_next();
-              if (!warp_wait_bounded(aux_bar(ew, (int)slot), (blk / GU) & 1u, p, lane)) { ok = false; break; }
-              add_block<OUT>(v, stg + slot * GU_BYTES, lane);
-            }
-            if (EPI == EPI_GRAD && p.residual != nullptr && m_ok && n0 < p.N) {
-              float r[32];
-              load_res32(r, p.residual, (long long)m * p.ldr, n0, p.N, p.res_dtype);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] += r[j];
-            }
-            if (p.scale != 1.0f) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] *= p.scale;
-            }
-          }
-          if constexpr (EPI != EPI_GLU_PART) {
-            if ((EPI == EPI_GLU || pair_a_mn(EPI)) && n0 + 32 > p.n_tma && n0 < p.N && m_ok) {
-              // ragged row end: a TMA store writes whole 16-byte granules
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (n0 + j >= p.n_tma && n0 + j < p.N) store_elem<OUT>(p.out, (long long)m * p.ldo + n0 + j, v[j]);
-            }
-            if constexpr (EPI == EPI_GRAD_ADD) {
-              const uint32_t at = stg + (blk % GU) * GU_BYTES;
-              put_block<OUT>(at, lane, v);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (inside) tma_store_2d(&tm0, at, n0, row);
-                bulk_commit_group();
+              for (int j = 0; j < 32; j += 2) {
+                float2 slope;
+                const float2 g = make_float2(__uint_as_float(ga[j]), __uint_as_float(ga[j + 1]));
+                const float2 h = mul2(gate2<ACT>(g, slope), make_float2(__uint_as_float(gu[j]), __uint_as_float(gu[j + 1])));
+                v[j] = h.x;
+                v[j + 1] = h.y;
               }
-              if constexpr (GU == 1) fetch_next();
-            } else {
-              emit(&tm0, n0, row, inside, v);
+              if constexpr (EPI == EPI_GLU) store_ragged(n0, m, m_ok, v);
+              emit(&tm0, n0, row, inside, lane, v);
             }
-          }
-        }
-        if (b + 1 == nblk) {
-          // this warp's TMEM reads of the tile are done: hand its share back to the leader
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (rank != 0) mbar_arrive_remote(mapa_shared(tempty_bar(buf), 0));
-            else mbar_arrive(tempty_bar(buf));
           }
         }
       }
       if (!ok) break;
+      hand_back(buf);
+      ++n;
       ++local;
       itm = nxt;
       more = have_next;
@@ -598,11 +681,6 @@ __device__ __forceinline__ float4 sum_splits(const float* w, long long split_str
     for (int k = 0; k < 8; ++k) a.x += t[k].x, a.y += t[k].y, a.z += t[k].z, a.w += t[k].w;
   }
   return a;
-}
-__device__ __forceinline__ float load_dt(const void* p, long long i, int dt) {
-  if (dt == DT_F32) return reinterpret_cast<const float*>(p)[i];
-  if (dt == DT_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(reinterpret_cast<const __half*>(p)[i]);
 }
 // four columns at element i (a multiple of four of a row that starts on 16 bytes), cnt of them inside
 __device__ __forceinline__ void load4_dt(float (&v)[4], const void* p, long long i, int dt, int cnt) {

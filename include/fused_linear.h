@@ -95,9 +95,10 @@ typedef enum { FL_COMPUTE_32F = 0, FL_COMPUTE_32F_3XTF32 = 1 } fl_compute;
  *                   residual (has_residual) is an earlier gradient to add to; it may be out's own
  *                   buffer, with the same type and pitch.  Sums are in fp32, in an order that
  *                   depends on the shape and the GPU alone.
- *                   The tensor cores' fp32 accumulators round towards zero, so that the error
- *                   grows with the tokens of one split: 4e-6 of the result's norm at 4096, 2e-5
- *                   at 16384 (the library's own 16-bit products measure the same).
+ *                   The tensor cores' accumulators round towards zero, so fp32 results are
+ *                   summed in runs of 896 tokens, and the runs rounded to nearest: an error of
+ *                   9e-7 of the result's norm whatever the tokens (random data).  16-bit results,
+ *                   whose own rounding is far coarser, are one sum: 4e-6 at 4096 tokens.
  * These take no bias, no unfused twin, FL_SCHED_AUTO only, and, but for WGRAD, no residual and no
  * scale. */
 typedef enum {
