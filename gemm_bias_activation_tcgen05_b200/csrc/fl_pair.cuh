@@ -68,12 +68,12 @@ constexpr int kPairRun = 896;
 // in x² that holds the constants.  Two values at a time: eight epilogue warps are few for the arithmetic
 // of a tile, and the packed fp32 instructions halve it.
 // act(x), and in `slope` act'(x) = σ + x·σ·(1 − σ)·y'(x).  x is held within ±200 where only σ's ends
-// matter: no 0·∞ for the largest values.
+// matter: no 0·∞ for the largest values.  A NaN stays one, in act and in act'.
 constexpr float kLog2E = 1.4426950408889634f, kTwoC = 2.0f * 0.79788456080286536f;
 template <int ACT>
 __device__ __forceinline__ float2 gate2(float2 x, float2& slope) {
   const float2 one = make_float2(1.0f, 1.0f), minus = make_float2(-1.0f, -1.0f);
-  const float2 xc = make_float2(fminf(fmaxf(x.x, -200.0f), 200.0f), fminf(fmaxf(x.y, -200.0f), 200.0f));
+  const float2 xc = make_float2(clamp_nan(x.x, 200.0f), clamp_nan(x.y, 200.0f));
   float2 arg, dy = one;
   if constexpr (ACT == GATE_SWIGLU) {
     arg = mul2(xc, make_float2(-kLog2E, -kLog2E));

@@ -319,6 +319,13 @@ __device__ __forceinline__ float tanh_approx(float x) {
   return y;
 }
 
+// x within ±b, NaN where x is (fminf and fmaxf would give the bound)
+__device__ __forceinline__ float clamp_nan(float x, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-b));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(b));
+  return y;
+}
 // two fp32 operations in one instruction, each rounded as the single one is
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;

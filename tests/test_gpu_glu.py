@@ -378,3 +378,26 @@ def test_a_training_step_of_the_block(fl, kind):
                                (dgam, tg.grad, 4, "dgamma"), (dbet, tb.grad, 1, "dbeta")]:
         rel = float((got.double().cpu() - want).norm() / want.norm())
         assert rel <= n * 2.0 ** -8, (what, rel)
+
+
+@pytest.mark.parametrize("kind", ["SWIGLU", "GEGLU_TANH"])
+@pytest.mark.parametrize("M,N,K,split", [(64, 64, 64, False), (300, 264, 200, False), (64, 1000, 4000, True)])
+def test_nan_gates_give_nan_gradients(fl, kind, M, N, K, split):
+    """act(NaN) and act'(NaN) are NaN: both gradients of such a place are, and no other place's is."""
+    dy, d_dy = mat(M, K, "bf16", 1, 0.5)
+    Wd, dW = mat(K, N, "bf16", 2, 1 / math.sqrt(N))
+    gu = torch.randn(M, 2 * N, generator=torch.Generator().manual_seed(3)).bfloat16()
+    nan = np.zeros((M, N), bool)
+    nan[::7, ::5] = nan[M - 1, N - 1] = nan[0, 1] = True
+    gu[:, :N][torch.from_numpy(nan)] = float("nan")
+    out = torch.zeros(M, 2 * N, dtype=torch.bfloat16, device="cuda")
+    info = run(fl, fl.Plan(M, N, K, kind=KIND[kind][2], out_dtype="bf16", b_major=1), d_dy, dW, aux=gu.cuda(), out=out)
+    assert (info["split_k"] > 1) == split
+    got = P.to64(out)
+    for name, half in (("dg", got[:, :N]), ("du", got[:, N:])):
+        assert np.array_equal(np.isnan(half), nan), name
+    clean = np.where(np.tile(nan, (1, 2)), 0.0, P.to64(gu))
+    both = np.concatenate([nan, nan], axis=1)
+    want, dh = T.glu_backward(dy, Wd, clean, kind)
+    assert (dh != 0).all()
+    assert np.abs(np.where(both, 0, got - want)).max() <= 2.0 ** -7 * np.abs(want).max()
