@@ -441,3 +441,45 @@ def test_forward_and_backward_in_one_graph_on_another_stream(fl):
                   seed, 0, ("bf16",) * 3, "graph")
     check_backward(dict(dres=P.to64(dres), dx=P.to64(dxo), dgamma=P.to64(dg), dbeta=P.to64(db)), P.to64(dz), None, P.to64(s),
                    P.to64(mean), P.to64(rstd), None, p, seed, 0, ("bf16",) * 3, "graph")
+
+
+# ---------------------------------------------------------------- rows that hold infinities
+@pytest.mark.parametrize("N", [96, 101, 768, 4096, 4099, 16384, 16400])
+@pytest.mark.parametrize("types", [("f32", "f32", "f32", "f32"), ("bf16", "f32", "f16", "f32")])
+def test_a_row_with_an_infinity_has_its_mean(fl, N, types):
+    """Row 1 holds +inf, row 2 -inf, row 3 both, row 4 a NaN: mean, rstd and z as the definition gives them, other rows as ever."""
+    M, xt, zt = 6, types[0], types[2]
+    x = draw((M, N), xt, N)
+    x[1, 3], x[2, N - 1], x[3, 0], x[3, N - 1], x[4, 5] = float("inf"), -float("inf"), float("inf"), -float("inf"), float("nan")
+    z = torch.zeros(M, N, dtype=P.TD[zt], device="cuda")
+    mean, rstd = (torch.zeros(M, device="cuda") for _ in range(2))
+    fl.fl_dropout_layernorm(x.cuda(), None, None, None, None, z, mean, rstd, M, N, *types, eps=1e-5)
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        _, z64, mean64, rstd64 = T.dropout_layernorm(P.to64(x), None, None, None, 1e-5)
+    assert np.isinf(mean64[1]) and np.isinf(mean64[2]) and np.isnan(mean64[3]) and np.isnan(mean64[4])
+    for got, want, what in ((mean, mean64, "mean"), (rstd, rstd64, "rstd"), (z, z64, "z")):
+        got = P.to64(got)
+        assert np.array_equal(np.isnan(got), np.isnan(want)), what
+        inf = np.isinf(want)
+        assert np.array_equal(got[inf], want[inf]) and np.isfinite(got[~inf & ~np.isnan(want)]).all(), what
+
+
+@pytest.mark.parametrize("N", [96, 101, 4096, 16400])
+def test_a_gradient_with_an_infinity_as_the_definition_gives_it(fl, N):
+    """dz of row 1 holds an infinity: infinite and NaN places of dres are the definition's, the other rows are as ever."""
+    M = 3
+    s, dz = draw((M, N), "f32", 1), draw((M, N), "f32", 2)
+    dz[1, 4] = float("inf")
+    s64 = P.to64(s)
+    mean, rstd = s64.mean(axis=1).astype(np.float32), (1 / np.sqrt(s64.var(axis=1) + 1e-5)).astype(np.float32)
+    dres = torch.zeros(M, N, device="cuda")
+    fl.fl_dropout_layernorm_backward(dz.cuda(), None, s.cuda(), torch.from_numpy(mean).cuda(), torch.from_numpy(rstd).cuda(), None,
+                                     dres, None, None, None, M, N, "f32", "f32", "f32")
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        want = T.dropout_layernorm_backward(P.to64(dz), None, s64, mean.astype(np.float64), rstd.astype(np.float64), None)[0]
+    got = P.to64(dres)
+    assert np.isinf(want[1]).any() and np.isnan(want[1]).any()
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+    assert np.isfinite(got[[0, 2]]).all()
