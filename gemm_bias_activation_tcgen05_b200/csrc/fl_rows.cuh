@@ -491,7 +491,9 @@ struct DropLnArgs {
 // T threads hold a row, V vectors of eight each (N ≤ 8·V·T): the row is read once, stays in
 // registers through the mean, Σ(s − μ)² and the normalisation, and every output is written once.
 // A CTA holds max(1, 128/T) rows at a time and walks the rows a grid apart; γ and β stay in registers
-// (but for 1024 threads, which have 64 each).  Three vectors need 150 to 168 registers: three CTAs of 128
+// (32 of them) but for 768 and 1024 threads, which have 80 and 64 each and read them from the cache at each
+// row: kept in registers they made the 768-thread kernels spill (4096 x 10240 f16 with an fp32 stream 127.8 us
+// against 113.8, 4096 x 12288 bf16 105.7 against 104.0, 64 rows of it 7.0 against 5.7).  Three vectors need 150 to 168 registers: three CTAs of 128
 // threads an SM (with four, 128 registers spilled: 16384 x 1536 with an fp32 stream 66.6 us against 50.2).
 __host__ __device__ constexpr int ln_block(int t) { return t < 128 ? 128 : t; }
 template <int T, int V, int XT, int ST, int ZT>
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(ln_block(T), V == 3 ? 3 : T <= 128 ? 4 : T == 
     fl_dropout_ln_kernel(const DropLnArgs P) {
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
-  constexpr bool TYPED = XT >= 0, HOIST = T < 1024;
+  constexpr bool TYPED = XT >= 0, HOIST = T < 768;
   constexpr int R = ln_block(T) / T;
   static_assert(R <= 15, "a row group has a named barrier of its own, 1 to 15");
   extern __shared__ __align__(16) uint8_t ring_s[];
