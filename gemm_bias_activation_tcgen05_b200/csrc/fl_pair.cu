@@ -34,6 +34,13 @@ template <int EPI, int ACT>
 PairFn by_out(int out, int atoms) {
   return out == FL_BF16 ? by_atoms<EPI, ACT, DT_BF16>(atoms) : by_atoms<EPI, ACT, DT_F16>(atoms);
 }
+// (128-deep stages only: a run is longer than the K loops that take 64-deep ones)
+template <int EPI>
+PairFn runs_kernel(int out) {
+  return out == FL_F32    ? &fl_pair_tcgen05<EPI, GATE_SWIGLU, DT_F32, 2>
+         : out == FL_BF16 ? &fl_pair_tcgen05<EPI, GATE_SWIGLU, DT_BF16, 2>
+                          : &fl_pair_tcgen05<EPI, GATE_SWIGLU, DT_F16, 2>;
+}
 PairFn pair_kernel(int epi, bool geglu, int out, int atoms) {
   switch (epi) {
     case EPI_GLU: return by_out<EPI_GLU, GATE_SWIGLU>(out, atoms);  // (GEGLU_TANH has kernels of its own)
@@ -44,8 +51,8 @@ PairFn pair_kernel(int epi, bool geglu, int out, int atoms) {
     case EPI_DGLU_PART: return by_atoms<EPI_DGLU_PART, GATE_SWIGLU, DT_F32>(atoms);
     case EPI_GRAD_ADD:  // (fp32: 64-deep stages only, see pair_config)
       return out == FL_F32 ? &fl_pair_tcgen05<EPI_GRAD_ADD, GATE_SWIGLU, DT_F32, 1> : by_out<EPI_GRAD_ADD, GATE_SWIGLU>(out, atoms);
-    case EPI_RUNS: return &fl_pair_tcgen05<EPI_RUNS, GATE_SWIGLU, DT_F32, 2>;
-    case EPI_RUNS_ADD: return &fl_pair_tcgen05<EPI_RUNS_ADD, GATE_SWIGLU, DT_F32, 2>;
+    case EPI_RUNS: return runs_kernel<EPI_RUNS>(out);
+    case EPI_RUNS_ADD: return runs_kernel<EPI_RUNS_ADD>(out);
     default:
       return out == FL_F32 ? by_atoms<EPI_GRAD, GATE_SWIGLU, DT_F32>(atoms) : by_out<EPI_GRAD, GATE_SWIGLU>(out, atoms);
   }
@@ -60,14 +67,14 @@ void (*finish_kernel(int kind))(FinishArgs) {
   }
 }
 // What the tile kernel itself computes and writes: with K splits, fp32 partial results.  The residual
-// of a weight gradient comes and leaves by TMA when the types agree.  Long sums are taken in runs for fp32
-// results (a 16-bit one is rounded a thousand times coarser than one sum is off).
+// of a weight gradient comes and leaves by TMA when the types agree.  Sums longer than the result's type
+// allows are taken in runs (pair_run), K splits' too.
 int kernel_epi(const fl_plan_s* p) {
   const int epi = epi_of(p->epi.kind);
   const bool split = p->split_k > 1;
   if (epi == EPI_DGLU) return split ? EPI_DGLU_PART : epi;
   if (epi != EPI_GRAD) return split ? EPI_GLU_PART : epi;
-  const bool runs = p->epi.out_dtype == FL_F32 && cdiv(cdiv(p->K, kPairBk), p->split_k) * kPairBk > kPairRun;
+  const bool runs = cdiv(cdiv(p->K, kPairBk), p->split_k) * kPairBk > pair_run(p->epi.out_dtype);
   const bool add = !split && p->epi.has_residual && p->epi.residual_dtype == p->epi.out_dtype;
   return runs ? (add ? EPI_RUNS_ADD : EPI_RUNS) : add ? EPI_GRAD_ADD : EPI_GRAD;
 }

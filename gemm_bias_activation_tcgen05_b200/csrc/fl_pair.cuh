@@ -54,12 +54,14 @@ __host__ __device__ constexpr bool pair_a_mn(int epi) {
 __host__ __device__ constexpr bool pair_b_mn(int epi) { return pair_a_mn(epi) || epi == EPI_DGLU || epi == EPI_DGLU_PART; }
 __host__ __device__ constexpr bool pair_glu(int epi) { return epi == EPI_GLU || epi == EPI_GLU_AUX || epi == EPI_GLU_PART; }
 
-// The tensor core's accumulators round towards zero, which costs an fp32 result 1e-9 of its norm for each
-// k of a sum: 4.4e-6 at 4096 tokens, 1.9e-5 at 16384.  So fp32 sums of more than 896 tokens (EPI_RUNS) are
-// taken in runs of 896, each in an accumulator of its own, which the epilogue warps add in registers,
-// rounded to nearest (half of the tile's columns a warp: 128 registers), while the next run is multiplied:
-// 9e-7 whatever the tokens.  A run costs 0.4 us a tile: 2048 x 2048 of 4096 tokens 25.6 -> 28 us.
-constexpr int kPairRun = 896;
+// The tensor core's accumulators round towards zero, which shrinks a sum by 1e-9 of its norm for each k: an
+// fp32 result is off by 4.4e-6 at 4096 tokens, 1.9e-5 at 16384.  So weight gradients of many tokens (EPI_RUNS) are
+// taken in runs, each in an accumulator of its own, which the epilogue warps add in fp32 registers, rounded to
+// nearest (half of the tile's columns a warp: 128 registers), while the next run is multiplied.  Runs of 896 tokens for fp32
+// results: 9e-7 whatever the tokens.  A run costs 0.4 us a tile: 2048 x 2048 of 4096 tokens 25.6 -> 28 us.
+// For 16-bit results the run is as long as leaves the shrinkage near a twentieth of the type's own rounding
+// (rms 2.1e-4 f16, 1.7e-3 bf16): 8192 tokens for f16 (8e-6), 65536 for bf16 (7e-5).
+__host__ __device__ constexpr int pair_run(int out) { return out == DT_F32 ? 896 : out == DT_F16 ? 8192 : 65536; }
 
 // The gates are x·σ(y): y = x (SWIGLU), or y = 2c(x + 0.044715x³), c = √(2/π), for the tanh GELU,
 // because (1 + tanh w)/2 = σ(2w): no cancellation for negative x, so that both keep fp32 precision over
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   constexpr bool GLU = pair_glu(EPI);
   constexpr bool A_MN = pair_a_mn(EPI), B_MN = pair_b_mn(EPI);
   constexpr bool SUMS = EPI == EPI_RUNS || EPI == EPI_RUNS_ADD;
-  constexpr int RUN = kPairRun / (ATOMS * kPairBk);  // stages of a run
+  constexpr int RUN = pair_run(OUT) / (ATOMS * kPairBk);  // stages of a run
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5;
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // RUNS_ADD takes the whole tile's residual into its sums at the tile's start, during the first run.
     constexpr bool IN_PLACE = EPI == EPI_DGLU || EPI == EPI_GRAD_ADD || EPI == EPI_RUNS_ADD;
     constexpr uint32_t GU_BYTES = EPI == EPI_GRAD_ADD || EPI == EPI_RUNS_ADD ? pair_block_bytes(OUT) : 4096u;
-    constexpr uint32_t GU = pair_warp_staging(ATOMS) / GU_BYTES < 2u ? 1u : 2u;
+    constexpr uint32_t GU = EPI == EPI_RUNS_ADD || pair_warp_staging(ATOMS) / GU_BYTES < 2u ? 1u : 2u;
     auto fetch_gu = [&](const PairItem& w, int b, uint32_t to) {
       const int n0 = w.tb * p.out_tile_n + c_begin + 32 * b, r0 = w.ta * 256 + (int)rank * 128 + q * 32;
       mbar_arrive_expect_tx(aux_bar(ew, (int)to), GU_BYTES);

@@ -95,10 +95,11 @@ typedef enum { FL_COMPUTE_32F = 0, FL_COMPUTE_32F_3XTF32 = 1 } fl_compute;
  *                   residual (has_residual) is an earlier gradient to add to; it may be out's own
  *                   buffer, with the same type and pitch.  Sums are in fp32, in an order that
  *                   depends on the shape and the GPU alone.
- *                   The tensor cores' accumulators round towards zero, so fp32 results are
- *                   summed in runs of 896 tokens, and the runs rounded to nearest: an error of
- *                   9e-7 of the result's norm whatever the tokens (random data).  16-bit results,
- *                   whose own rounding is far coarser, are one sum: 4e-6 at 4096 tokens.
+ *                   The tensor cores' accumulators round towards zero, which shrinks a sum by 1e-9 of its
+ *                   norm for each token.  So sums are taken in runs, and the runs rounded to nearest: of
+ *                   896 tokens for fp32 results, an error of 9e-7 of the result's norm whatever the
+ *                   tokens (random data); of 8192 for f16 and 65536 for bf16 results, 8e-6 and 7e-5, near
+ *                   a twentieth of the error of rounding to these types.
  * These take no bias, no unfused twin, FL_SCHED_AUTO only, and, but for WGRAD, no residual and no
  * scale. */
 typedef enum {

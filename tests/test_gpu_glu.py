@@ -427,3 +427,42 @@ def test_long_fp32_sums_hold_the_error_of_a_run(fl, M, N, tokens, split_tokens, 
     assert -(-tokens // info["split_k"]) == (split_tokens or tokens)
     rel = float((got - want).norm() / want.norm())
     assert rel < 1.3e-6, rel
+
+
+@pytest.mark.parametrize("M,N,tokens,split_tokens,dtype,out_dtype", [
+    (2304, 2304, 131072, 0, "f16", "f16"), (2304, 2304, 262144, 0, "bf16", "bf16"), (512, 512, 262144, 14564, "f16", "f16")])
+@pytest.mark.parametrize("res_dtype", [None, "out", "f32"])
+def test_long_16_bit_sums_are_not_biased(fl, M, N, tokens, split_tokens, dtype, out_dtype, res_dtype):
+    """Accumulators that round towards zero shrink a sum by up to 1.1e-9 a token.  Sums are taken in runs of at most 8192
+    (f16) or 65536 (bf16) tokens, so the result is shrunk by at most 9e-6 or 7.2e-5; the rounding of 300 x N results to their own
+    type (2.1e-4 or 1.7e-3 rms) moves the mean by four deviations, 1e-6 or 8e-6, at most.  One sum would shrink by 1.4e-4 of
+    131072 tokens, 2.9e-4 of 262144."""
+    got, want, info = _long_sum(fl, M, N, tokens, dtype, out_dtype, out_dtype if res_dtype == "out" else res_dtype)
+    assert -(-tokens // info["split_k"]) == (split_tokens or tokens)
+    shrink = float(((got - want) * want).sum() / (want * want).sum())
+    assert abs(shrink) < (1e-5 if out_dtype == "f16" else 8e-5), shrink
+
+
+@pytest.mark.parametrize("tokens,dtype", [(8300, "f16"), (65700, "bf16")])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_long_16_bit_sums_of_ragged_weights(fl, tokens, dtype, accumulate):
+    """Just past one run, odd sizes and pitches, the earlier gradient in place: every element, and nothing between the rows.
+    The bound of an accumulator of K products (above), two roundings to nearest and the result's own."""
+    M, N, ld = 2101, 2099, 2104
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    dy, x = (torch.full((tokens, ld), float("nan"), dtype=P.TD[dtype], device="cuda") for _ in range(2))
+    for t, c in ((dy, M), (x, N)):
+        t[:, :c] = torch.randn(tokens, c, generator=gen, device="cuda").to(P.TD[dtype])
+    out = torch.full((M, ld), float("nan"), dtype=P.TD[dtype], device="cuda")
+    a, b = dy[:, :M].double(), x[:, :N].double()
+    want, size = a.T @ b, a.abs().T @ b.abs()
+    if accumulate:
+        out[:, :N] = (50 * torch.randn(M, N, generator=gen, device="cuda")).to(P.TD[dtype])
+        want += out[:, :N].double()
+        size += out[:, :N].double().abs()
+    info = run(fl, fl.Plan(M, N, tokens, dtype=dtype, kind="WGRAD", b_major=1, out_dtype=dtype, has_residual=accumulate,
+                           residual_dtype=dtype, lda=ld, ldb=ld, ldo=ld, ldr=ld), dy, x, residual=out if accumulate else None, out=out)
+    assert info["split_k"] == 1 and info["stages"] == 3
+    within(P.to64(out[:, :N]), want.cpu().numpy(), ((tokens / 16 + 16) * 2 * E * size).cpu().numpy() + 2 * E * np.abs(want.cpu().numpy()),
+           dtype, f"{tokens} tokens")
+    assert torch.isnan(out[:, N:].float()).all()
