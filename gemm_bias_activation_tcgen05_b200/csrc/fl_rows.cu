@@ -202,7 +202,8 @@ extern "C" fl_status fl_dropout(const void* x, const void* residual, void* y, in
                                 const fl_dropout_desc* drop, void* stream_) {
   clear_error();
   const char* who = "fl_dropout";
-  if (!x || !y) return fail(FL_ERR_INVALID_ARG, "%s: null x or y", who);
+  const bool empty = M == 0 || N == 0;
+  if (!empty && (!x || !y)) return fail(FL_ERR_INVALID_ARG, "%s: null x or y", who);
   fl_status st = check_shape(who, M, N);
   if (st) return st;
   if (!is_dtype(x_dtype) || !is_dtype(y_dtype)) return fail(FL_ERR_INVALID_ARG, "%s: unknown dtype", who);
@@ -213,7 +214,7 @@ extern "C" fl_status fl_dropout(const void* x, const void* residual, void* y, in
       (st = check_operand(who, {"residual", residual, ld_r, y_dtype}, N, &P.r, &P.vec)) ||
       (st = check_operand(who, {"y", y, ld_y, y_dtype}, N, &P.y, &P.vec)))
     return st;
-  if (M == 0 || N == 0) return FL_OK;
+  if (empty) return FL_OK;
   P.M = M;
   P.N = (int)N;
   P.nvec = (int)cdiv(N, 8);
@@ -243,7 +244,8 @@ extern "C" fl_status fl_dropout_layernorm(const void* x, const void* residual, c
                                           const fl_dropout_desc* drop, void* stream_) {
   clear_error();
   const char* who = "fl_dropout_layernorm";
-  if (!x || !z) return fail(FL_ERR_INVALID_ARG, "%s: null x or z", who);
+  const bool empty = M == 0 || N == 0;
+  if (!empty && (!x || !z)) return fail(FL_ERR_INVALID_ARG, "%s: null x or z", who);
   if ((mean == nullptr) != (rstd == nullptr)) return fail(FL_ERR_INVALID_ARG, "%s: mean and rstd go together", who);
   fl_status st = check_shape(who, M, N);
   if (st) return st;
@@ -262,7 +264,7 @@ extern "C" fl_status fl_dropout_layernorm(const void* x, const void* residual, c
     return st;
   if (reinterpret_cast<uintptr_t>(mean) % 4 || reinterpret_cast<uintptr_t>(rstd) % 4)
     return fail(FL_ERR_ALIGNMENT, "%s: mean or rstd is not 4-byte aligned", who);
-  if (M == 0 || N == 0) return FL_OK;
+  if (empty) return FL_OK;
   P.gamma = gamma;
   P.beta = beta;
   P.mean = mean;
@@ -307,8 +309,10 @@ extern "C" fl_status fl_dropout_layernorm_backward(
     int32_t param_dtype, const fl_dropout_desc* drop, void* workspace, size_t workspace_bytes, void* stream_) {
   clear_error();
   const char* who = "fl_dropout_layernorm_backward";
-  if (!dz || !sum || !mean || !rstd) return fail(FL_ERR_INVALID_ARG, "%s: null dz, sum, mean or rstd", who);
-  if (!dres && !dx && !dgamma && !dbeta) return fail(FL_ERR_INVALID_ARG, "%s: no output", who);
+  const bool empty = M == 0 || N == 0;
+  if (!empty && (!dz || !sum || !mean || !rstd))
+    return fail(FL_ERR_INVALID_ARG, "%s: null dz, sum, mean or rstd", who);
+  if (!empty && !dres && !dx && !dgamma && !dbeta) return fail(FL_ERR_INVALID_ARG, "%s: no output", who);
   fl_status st = check_shape(who, M, N);
   if (st) return st;
   if (!is_dtype(x_dtype) || !is_dtype(sum_dtype) || !is_dtype(z_dtype) || !is_dtype(param_dtype))
@@ -325,6 +329,12 @@ extern "C" fl_status fl_dropout_layernorm_backward(
     return st;
   for (const void* p : {(const void*)mean, (const void*)rstd, (const void*)dgamma, (const void*)dbeta})
     if (reinterpret_cast<uintptr_t>(p) % 4) return fail(FL_ERR_ALIGNMENT, "%s: an fp32 vector is not 4-byte aligned", who);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  if (empty) {
+    for (float* q : {dgamma, dbeta})
+      if (q && N > 0) FL_CUDA(cudaMemsetAsync(q, 0, (size_t)N * sizeof(float), s));
+    return FL_OK;
+  }
   int sms = 148;
   if ((st = num_sms(&sms))) return st;
   // (the geometry, and so the workspace, does not depend on the types)
@@ -333,12 +343,6 @@ extern "C" fl_status fl_dropout_layernorm_backward(
   if (params && (!workspace || workspace_bytes < g.bytes || !aligned16(workspace)))
     return fail(FL_ERR_INVALID_ARG, "%s: dgamma and dbeta need a 16-byte aligned workspace of %zu bytes "
                 "(fl_layernorm_grad_workspace_size)", who, g.bytes);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
-  if (M == 0 || N == 0) {
-    for (float* q : {dgamma, dbeta})
-      if (q && N > 0) FL_CUDA(cudaMemsetAsync(q, 0, (size_t)N * sizeof(float), s));
-    return FL_OK;
-  }
   P.mean = mean;
   P.rstd = rstd;
   P.gamma = gamma;

@@ -271,6 +271,8 @@ typedef struct {
  *   x [M, ld_x] of x_dtype; residual (or null) [M, ld_r] and y [M, ld_y] of y_dtype; ld 0 = N.
  *   y may be x's or the residual's own buffer with the same type and pitch.
  * Any alignment of the elements is accepted; rows that all start on 16 bytes run fastest.
+ * M = 0 or N = 0, here and in the two below: nothing to do, and null operands are accepted (an empty
+ * tensor has no address).
  * Errors: FL_ERR_INVALID_ARG (null x or y, size, ld < N, dtype, p outside [0, 1)),
  * FL_ERR_ALIGNMENT, FL_ERR_CUDA. */
 fl_status fl_dropout(const void* x, const void* residual, void* y, int64_t M, int64_t N, int64_t ld_x, int64_t ld_r,
@@ -302,7 +304,7 @@ fl_status fl_dropout_layernorm(const void* x, const void* residual, const void* 
  *   [M]: from the forward pass (for a plain LayerNorm, sum is its input x); gamma as there.
  *   dres [M, ld_dres] of sum_dtype, dx [M, ld_dx] of x_dtype, dgamma, dbeta [N] fp32: each may
  *   be null (not wanted), not all.  dres and dx may each be dz's, dsum's or sum's own buffer with
- *   the same type and pitch (not both the same one).  M = 0 gives dgamma = dbeta = 0.
+ *   the same type and pitch (not both the same one).  M = 0 gives dgamma = dbeta = 0, without a workspace.
  *   workspace: needed for dgamma and dbeta; fl_layernorm_grad_workspace_size bytes (for the
  *   current device; never less for more rows), 16-byte aligned, owned by the caller, no initial contents needed.  Calls
  *   that overlap on the GPU must not share it.

@@ -483,3 +483,15 @@ def test_a_gradient_with_an_infinity_as_the_definition_gives_it(fl, N):
     assert np.isinf(want[1]).any() and np.isnan(want[1]).any()
     assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
     assert np.isfinite(got[[0, 2]]).all()
+
+
+def test_a_step_of_an_empty_batch(fl):
+    """No rows: every call succeeds on torch's empty tensors, whose address is null, and the parameters' gradients are 0."""
+    N, e = 264, torch.empty(0, 264, device="cuda")
+    v = torch.empty(0, device="cuda")
+    dgamma, dbeta = (torch.full((N,), float("nan"), device="cuda") for _ in range(2))
+    fl.fl_dropout(e, e, e, 0, N, "f32", "f32", p=0.1, seed=1)
+    fl.fl_dropout_layernorm(e, e, None, None, e, e, v, v, 0, N, "f32", "f32", "f32", p=0.1, seed=1)
+    fl.fl_dropout_layernorm_backward(e, e, e, v, v, None, e, e, dgamma, dbeta, 0, N, "f32", "f32", "f32", p=0.1, seed=1)
+    torch.cuda.synchronize()
+    assert not dgamma.any() and not dbeta.any()

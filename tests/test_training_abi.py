@@ -150,3 +150,16 @@ def test_pair_configurations(fl, kind):
             assert i.smem_bytes <= 232448 and i.stages >= 3 and i.grid % 2 == 0 and 0 < i.grid <= 148
             assert 1 <= i.split_k <= max(1, -(-K // 64)) and (i.split_k == 1 or i.split_k * -(-M // 256) * -(-N // i.tile_n) <= 148)
         assert i.launches_per_execute == (2 if i.split_k > 1 else 1)
+
+
+@pytest.mark.parametrize("M,N", [(0, 8), (8, 0), (0, 0)])
+def test_empty_matrices_have_no_addresses(fl, M, N):
+    """The pointer of an empty tensor is null: an empty batch is no error."""
+    none = dict(M=M, N=N)
+    assert _dropout(fl, x=None, y=None, **none) == fl.FL_OK, fl.fl_last_error()
+    assert _forward(fl, x=None, z=None, **none) == fl.FL_OK, fl.fl_last_error()
+    assert _backward(fl, dz=None, s=None, mean=None, rstd=None, dres=None, **none) == fl.FL_OK, fl.fl_last_error()
+    # what is wrong stays wrong
+    assert _dropout(fl, x=None, y=None, M=M, N=N, xt=9) == fl.FL_ERR_INVALID_ARG
+    assert _forward(fl, x=None, z=None, M=M, N=N, eps=-1.0) == fl.FL_ERR_INVALID_ARG
+    assert _dropout(fl, x=None, y=None, M=-1, N=N) == fl.FL_ERR_INVALID_ARG
