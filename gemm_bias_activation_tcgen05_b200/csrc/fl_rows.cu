@@ -24,10 +24,7 @@ fl_status drop_params(const char* who, const fl_dropout_desc* d, DropParams* out
   if (d->reserved != 0) return fail(FL_ERR_INVALID_ARG, "%s: reserved fields must be 0", who);
   if (reinterpret_cast<uintptr_t>(d->offset_dev) % 8)
     return fail(FL_ERR_ALIGNMENT, "%s: offset_dev must be 8-byte aligned", who);
-  for (uint32_t r = 0; r < 10; ++r) {
-    out->k0[r] = (uint32_t)d->seed + r * 0x9E3779B9u;
-    out->k1[r] = (uint32_t)(d->seed >> 32) + r * 0xBB67AE85u;
-  }
+  set_drop_keys(out, d->seed);
   out->offset = d->offset;
   out->offset_dev = d->offset_dev;
   out->threshold = (uint32_t)((double)d->p * 4294967296.0);  // ⌊p·2^32⌋ (p < 1: below 2^32)

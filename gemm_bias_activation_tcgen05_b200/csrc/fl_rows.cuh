@@ -34,6 +34,12 @@ struct DropParams {
   float scale;                 // 1/(1 − p)
   int on;                      // 0: p = 0, nothing is drawn
 };
+inline void set_drop_keys(DropParams* d, uint64_t seed) {
+  for (uint32_t r = 0; r < 10; ++r) {
+    d->k0[r] = (uint32_t)seed + r * 0x9E3779B9u;
+    d->k1[r] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
+  }
+}
 
 // What a thread keeps of the offset and the keys: everything that the first two rounds make of
 // them alone, for blocks below 2^32 (so that 18 multiplications remain of 20).
@@ -41,7 +47,7 @@ struct DropOffset {
   uint32_t w0, w1, w2;      // round 1: shares of the new words 0, 1 and 2
   uint32_t v0, v2, v3;      // round 2: shares of the new words 0, 2 and 3
 };
-__device__ __forceinline__ DropOffset drop_offset(const DropParams& d) {
+__host__ __device__ __forceinline__ DropOffset drop_offset(const DropParams& d) {
   uint64_t off = d.offset;
   if (d.on && d.offset_dev != nullptr) off += *d.offset_dev;
   const uint64_t b = (uint64_t)(uint32_t)off * 0xCD9E8D57u;
@@ -58,7 +64,7 @@ __device__ __forceinline__ DropOffset drop_offset(const DropParams& d) {
 
 // BIG: blocks may reach 2^32 (matrices of 2^34 elements and more, which run on the untyped kernels)
 template <bool BIG>
-__device__ __forceinline__ uint4 philox4x32_10(uint64_t block, const DropOffset& o, const DropParams& d) {
+__host__ __device__ __forceinline__ uint4 philox4x32_10(uint64_t block, const DropOffset& o, const DropParams& d) {
   const uint64_t first = (uint64_t)(uint32_t)block * 0xD2511F53u;
   const uint32_t f2 = (uint32_t)(first >> 32) ^ o.w2, f3 = (uint32_t)first;
   const uint64_t second = (uint64_t)f2 * 0xCD9E8D57u;

@@ -1,6 +1,10 @@
 """CPU pins of oracle/training.py: published vectors, finite differences, torch in float64."""
 from __future__ import annotations
 
+import os
+import shutil
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -88,3 +92,29 @@ def test_gated_block_gradients_against_differences(kind):
         f = lambda a, i=i, args=args: loss(*[a if j == i else args[j] for j in range(3)])  # noqa: E731
         assert abs(_diff(f, args[i], d) - (g * d).sum()) < 1e-6
     assert np.allclose(T.weight_grad(dy, h, Wd, 0.5), 0.5 * (dy.T @ h + Wd))
+
+
+def test_the_kernels_generator_on_the_host(tmp_path):
+    """The row kernels' own generator, whose first two rounds are folded, compiled for the host by nvcc: the published vectors,
+    and random counters and keys; blocks from 2^32 on (matrices of 2^34 elements) in the form that holds their high half."""
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("needs nvcc")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = tmp_path / "philox_check"
+    r = subprocess.run([nvcc, "-std=c++17", "-O1", "-gencode", "arch=compute_100a,code=sm_100a",
+                        os.path.join(root, "tests", "c", "philox_check.cu"), "-o", str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    rng = np.random.default_rng(5)
+    words = [int(v) for v in rng.integers(0, 2**64, 300, dtype=np.uint64)]
+    cases = [(big, block >> (0 if big else 32), seed, off) for big in (0, 1)
+             for block, seed, off in zip(words[::3], words[1::3], words[2::3])]
+    cases += [(0, 0, 0, 0), (1, 0, 0, 0), (1, 2**64 - 1, 2**64 - 1, 2**64 - 1), (1, 2**32, 7, 9), (1, 2**32 - 1, 7, 9), (0, 2**32 - 1, 7, 9),
+              (1, 0x85A308D3243F6A88, 0x299F31D0A4093822, 0x0370734413198A2E)]
+    r = subprocess.run([str(exe)], input="\n".join(" ".join(map(str, c)) for c in cases), capture_output=True, text=True, timeout=120)
+    got = [tuple(map(int, line.split())) for line in r.stdout.splitlines()]
+    assert r.returncode == 0 and len(got) == len(cases)
+    half = 0xFFFFFFFF
+    for (big, block, seed, off), words4 in zip(cases, got):
+        want = T.philox4x32((block & half, block >> 32, off & half, off >> 32), (seed & half, seed >> 32))
+        assert words4 == tuple(int(v) for v in want), (big, hex(block), hex(seed), hex(off))
