@@ -111,7 +111,7 @@ struct KParams {
   float inv_group;  // 1 / (8 * tiles_b): the tile raster's group size, inverted on the host
   float* sk_ws;   // fp32 partial accumulators: [cluster][CTA rank][epilogue warp][mma_n/2 x 32]
   int* sk_flags;  // [cluster][CTA rank][epilogue warp]: 1 once that warp's partial is stored
-  int split_rows;  // weight gradient with K splits: workspace rows of one split
+  int split_rows;  // fl_pair.cuh with K splits: workspace rows of one split
 };
 
 // ------------------------------------------------------------------ work schedule

@@ -5,7 +5,7 @@
 //   EPI_GLU      h = act(A·Wgᵀ) ⊙ (A·Wuᵀ)                       W = [Wg; Wu] stacked, K contiguous
 //   EPI_GLU_AUX  the same, and g = A·Wgᵀ, u = A·Wuᵀ stored for the backward pass
 //   EPI_DGLU     dh = A·W (W stored [K, N]), then dg = dh·u·act'(g), du = dh·act(g) from the
-//                stored g, u: dh never leaves the chip
+//                stored g, u: dh never leaves the chip (but as the fp32 partial sums of K splits)
 //   EPI_GRAD     y = (Aᵀ·W + residual)·scale, A stored [K, M] and W stored [K, N]: the weight
 //                gradient, K the tokens.  Both operands are read as they lie, through MN-major UMMA
 //                descriptors, so nothing is transposed in memory.

@@ -86,7 +86,8 @@ typedef enum { FL_COMPUTE_32F = 0, FL_COMPUTE_32F_3XTF32 = 1 } fl_compute;
  *                   the backward through the gate, fused into the product that brings the
  *                   gradient: A = dy [M, K], W = the down projection's weight stored [K, N]
  *                   (b_major 1), aux = the forward's [M, 2N], read only; with dh = A·W, which is
- *                   never stored or rounded, out [M, ldo], ldo ≥ 2N (0: 2N), is
+ *                   never rounded below fp32 (and stays on the chip but for K splits, whose fp32
+ *                   partial sums pass through the workspace), out [M, ldo], ldo ≥ 2N (0: 2N), is
  *                   [dh·u·act'(g), dh·act(g)]; N a multiple of 8.  out may be aux's own buffer
  *                   when ldo is 2N.  (The gradient of the block's input is then the NONE layer
  *                   out·[Wg; Wu] with b_major 1 and 2N as its K.)
@@ -100,6 +101,10 @@ typedef enum { FL_COMPUTE_32F = 0, FL_COMPUTE_32F_3XTF32 = 1 } fl_compute;
  *                   896 tokens for fp32 results, an error of 9e-7 of the result's norm whatever the
  *                   tokens (random data); of 8192 for f16 and 65536 for bf16 results, 8e-6 and 7e-5, near
  *                   a twentieth of the error of rounding to these types.
+ * The sums over K of the gated kinds run in one accumulator each (several for K splits and few rows): they
+ * are shrunk by 1e-9 of their norm for each k, 4e-6 at K = 4096, where rounding to f16 costs 2e-4.
+ * GEGLU_TANH takes the hardware's tanh (relative error 2^-11), GEGLU_TANH_AUX and DGEGLU_TANH x·σ(y) in
+ * fp32 precision, so that h may differ in its last bits between serving and training.
  * These take no bias, no unfused twin, FL_SCHED_AUTO only, and, but for WGRAD, no residual and no
  * scale. */
 typedef enum {
@@ -161,8 +166,9 @@ typedef struct fl_plan_s* fl_plan_t;
  * of an unfused plan; and, when the shape's tiles leave the last round of CTA pairs
  * partly idle (16-bit operands, M > 128), the stream-K workspace: one fp32 partial
  * accumulator of 32 rows x mma_n/2 columns per CTA and epilogue warp (at most
- * 148 x 8 x 16 KB = 19.4 MB on a B200) and its flags; for WGRAD, when its tiles would leave CTA
- * pairs idle, the fp32 partial results of up to 32 K splits.  Every execute of the plan
+ * 148 x 8 x 16 KB = 19.4 MB on a B200) and its flags; for the kinds SWIGLU to WGRAD, when their
+ * tiles would leave CTA pairs idle, the fp32 partial results of up to 32 K splits
+ * (launches_per_execute of fl_plan_info is then 2).  Every execute of the plan
  * reuses this workspace, so two executes of one plan must not overlap on the GPU.
  * Needs the target device current.
  *   out     receives the plan handle (host pointer, must not be NULL)
@@ -174,7 +180,7 @@ fl_status fl_plan(fl_plan_t* out, int64_t M, int64_t N, int64_t K, int32_t dtype
                   int32_t compute, const fl_epilogue_desc* epi);
 
 /* Run the planned layer on `stream` (a cudaStream_t; NULL = legacy default stream)
- * ([epilog] execute(): one kernel launch for a fused plan).
+ * ([epilog] execute(): one kernel launch for a fused plan; two where SWIGLU to WGRAD split K).
  *   A        [M, lda] operand
  *   W        [N, ldb] weight (b_major 0), [K, ldb] (b_major 1) or [2N, ldb] (GEGLU, SWIGLU)
  *   bias     length N (bias_axis 0) or M (bias_axis 1); required iff the kind has a bias
@@ -329,7 +335,7 @@ typedef struct {
   int32_t tile_m, tile_n;      /* output tile of one CTA (before split-K) */
   int32_t mma_n;               /* tensor-core N per instruction */
   int32_t swap_ab;             /* 1: W is the tensor-core A operand (small M) */
-  int32_t split_k;             /* CTAs of a cluster sharing one tile along K; WGRAD: splits of K */
+  int32_t split_k;             /* CTAs of a cluster sharing one tile along K; SWIGLU to WGRAD: splits of K */
   int32_t stages;              /* shared-memory pipeline depth */
   int32_t grid;                /* CTAs launched by the main kernel */
   int32_t smem_bytes;          /* dynamic shared memory per CTA */
@@ -378,7 +384,8 @@ const char* fl_last_error(void);
  *   - The error word is cleared at each call and not read back: a bounded
  *     in-kernel wait that gives up is not reported by this entry point.
  *   - fp16/bf16 operands with FL_COMPUTE_32F only.
- *   - WGRAD runs without K splits, which need a workspace: slower when it has few tiles.
+ *   - SWIGLU to WGRAD run without K splits, which need a workspace: slower where fl_plan would
+ *     split, and their sums then run in another order than a plan's.
  * Errors: as fl_plan and fl_execute. */
 fl_status fl_execute_noalloc(int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t compute,
                              const fl_epilogue_desc* epi, const void* A, const void* W,
