@@ -139,17 +139,21 @@ fl_status fl::host::pair_config(fl_plan_s* p, bool no_workspace) {
   double best = 1e300;
   for (int width : {256, 128}) {
     const int64_t tiles = cdiv(p->M, 256) * cdiv(p->N, glu ? width / 2 : width);
-    // microseconds of a 64-deep K block, and of what a unit adds outside its K loop
+    // microseconds of a 64-deep K block, and of what a unit adds outside its K loop.  Measured: a block 0.41
+    // 256 wide and 0.26 to 0.34 128 wide; beside its blocks the first round 5, each further one about 1, for
+    // which 2.5 a round stands.  The times of one short round come out 1.8 times the estimate, of seven rounds
+    // 0.8 times, of long K loops and of K splits 1.0 to 1.2 times.  The epilogue of the backward through the gate
+    // (up to 8 us more a round) and the runs of long sums (0.4 us each) are not in it.
     const double block_us = width == 256 ? 0.40 : 0.30, unit_us = 2.5;
     const int most = no_workspace ? 1 : std::min(p->num_kb, 32);
     for (int S = 1; S <= std::max(1, most); ++S) {
       const int64_t units = tiles * S;
       if (units >= (1LL << 24) || (S > 1 && units > 2 * P)) break;  // (the tile raster's range; the workspace's size)
       double us = (double)cdiv(units, P) * ((double)cdiv(p->num_kb, S) * block_us + unit_us);
-      // every operand comes from memory once, by the SMs that are busy
+      // every operand comes from memory once (6 TB/s of the copy's 6.5), by the SMs that are busy
       const double bytes = 2.0 * (M * K + cols * K + (epi == EPI_GRAD ? 2.0 : 3.0) * M * N);
       us = std::max(us, bytes / (6.0e6 * std::min(1.0, (double)units / (double)P)));
-      // the partial results are written and read once more (mostly in L2), by one more launch
+      // the partial results are written and read once more (mostly in L2, at about 8 TB/s), by one more launch (3.5)
       if (S > 1) us += 3.5 + (double)S * 8.0 * M * cols / 8e6;
       if (us < best) {
         best = us;

@@ -151,9 +151,10 @@ RowKernel<DropLnBwdArgs> ln_bwd_kernel(int64_t M, int64_t N, int sms, RowTypes r
 
 // Launch geometry of the backward pass: CTAs (each leaves one partial row of dγ and one of dβ)
 // and the pitch of those rows.  One CTA per SM: a second one would halve the registers of each thread,
-// and the loop, which then keeps fewer loads and draws under way, measured slower with it (8192 x 4096
-// bf16: 87.7 us with two CTAs of 121 registers a thread, 75.5 with one of 160), and would leave twice
-// as many partial rows.
+// and the loop, which then keeps fewer loads and draws under way, measured slower with it at every width,
+// and would leave twice as many partial rows.  One against two, in us: 8192 x 4096 bf16 78.0 (158 registers) and
+// 85.0 (124), with an fp32 stream 89.4 and 96.3, in fp32 108.5 and 113.8; 8192 x 2048 44.1 and 51.3; 2048 x 768 9.1
+// and 12.1; 32768 x 768 52.4 and 80.1; 4096 x 8192 77.6 and 133.
 struct BwdGeom {
   RowKernel<DropLnBwdArgs> k;
   int grid, ws_ld;
