@@ -58,7 +58,7 @@ __host__ __device__ constexpr bool pair_glu(int epi) { return epi == EPI_GLU || 
 // fp32 result is off by 4.4e-6 at 4096 tokens, 1.9e-5 at 16384.  So weight gradients of many tokens (EPI_RUNS) are
 // taken in runs, each in an accumulator of its own, which the epilogue warps add in fp32 registers, rounded to
 // nearest (half of the tile's columns a warp: 128 registers), while the next run is multiplied.  Runs of 896 tokens for fp32
-// results: 9e-7 whatever the tokens.  A run costs 0.4 us a tile: 2048 x 2048 of 4096 tokens 25.6 -> 28 us.
+// results: 9e-7 whatever the tokens (f16 operands, whose products have more bits: 1.1e-6).  A run costs 0.4 us a tile: 2048 x 2048 of 4096 tokens 25.6 -> 28 us.
 // For 16-bit results the run is as long as leaves the shrinkage near a twentieth of the type's own rounding
 // (rms 2.1e-4 f16, 1.7e-3 bf16): 8192 tokens for f16 (8e-6), 65536 for bf16 (7e-5).
 __host__ __device__ constexpr int pair_run(int out) { return out == DT_F32 ? 896 : out == DT_F16 ? 8192 : 65536; }

@@ -466,3 +466,12 @@ def test_long_16_bit_sums_of_ragged_weights(fl, tokens, dtype, accumulate):
     within(P.to64(out[:, :N]), want.cpu().numpy(), ((tokens / 16 + 16) * 2 * E * size).cpu().numpy() + 2 * E * np.abs(want.cpu().numpy()),
            dtype, f"{tokens} tokens")
     assert torch.isnan(out[:, N:].float()).all()
+
+
+@pytest.mark.parametrize("M,N,tokens", [(536, 4016, 1770), (2304, 2304, 16384), (512, 512, 131072)])
+def test_long_fp32_sums_of_f16_hold_the_error_of_a_run(fl, M, N, tokens):
+    """f16 products have 22 bits where bf16's have 16, of which the accumulator keeps fewer: the documented 1.1e-6 of a run, with
+    the additions' 3.6e-7 (as above) 1.16e-6, so below 1.3e-6."""
+    got, want, _ = _long_sum(fl, M, N, tokens, "f16", "f32")
+    rel = float((got - want).norm() / want.norm())
+    assert rel < 1.3e-6, rel
