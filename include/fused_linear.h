@@ -99,8 +99,9 @@ typedef enum { FL_COMPUTE_32F = 0, FL_COMPUTE_32F_3XTF32 = 1 } fl_compute;
  *                   The tensor cores' accumulators round towards zero, which shrinks a sum by 1e-9 of its
  *                   norm for each token.  So sums are taken in runs, and the runs rounded to nearest: of
  *                   896 tokens for fp32 results, an error of 9e-7 of the result's norm (1.1e-6 with f16
- *                   operands) whatever the tokens (random data); of 8192 for f16 and 65536 for bf16 results, 8e-6 and 7e-5, near
- *                   a twentieth of the error of rounding to these types.
+ *                   operands) whatever the tokens (random data); of 8192 for f16 and
+ *                   65536 for bf16 results, shrunk by 8e-6 and 7e-5, near a twentieth of what
+ *                   rounding to these types costs.
  * The sums over K of the gated kinds run in one accumulator each (several for K splits and few rows): they
  * are shrunk by 1e-9 of their norm for each k, 4e-6 at K = 4096, where rounding to f16 costs 2e-4.
  * GEGLU_TANH takes the hardware's tanh (relative error 2^-11), GEGLU_TANH_AUX and DGEGLU_TANH x·σ(y) in
